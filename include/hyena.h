@@ -365,6 +365,76 @@ int hyena_nd_film_fwd_profiled(int X, int Y, int Z, int C, int N, int boundary, 
                                float *k_out, void *ws, size_t ws_bytes, hipStream_t stream,
                                const hipEvent_t *events);
 
+/* ------------------------------------------- gated linear recurrence ---- */
+/*
+ * The other data-controlled mixer over [B][L][D] beside the long convolution:
+ * a recurrence with a state of one value per channel, computed as a scan over
+ * the sequence, and served one position at a time. Per sample b and channel d:
+ *   a_t = sigmoid(f_t + bias),  h_t = a_t h_{t-1} + (1 - a_t) v_t,  h_{-1} = h0
+ *   y_t = h_t silu(g_t)          (y_t = h_t if g is NULL)
+ *  - reset[b][t] != 0: the history ends before t, h_t = (1 - a_t) v_t. Nothing of
+ *    the positions before t reaches t, not even an infinity or NaN.
+ *  - t >= lens[b] (clamped to [0, L]): padding. It is not part of the sequence:
+ *    what v, f, g, dy and reset hold there is not used, the state stays that of
+ *    position lens[b] - 1 (h0 if lens[b] = 0), and y is left as it was.
+ * Element (b, t, d) of v lies at v + b v_batch + t v_row + d, and likewise for the
+ * others, so v, f and g may be column blocks of one projection's output. Rows are
+ * contiguous; every stride is a multiple of 8 (bf16) or 4 (fp32) elements and not
+ * negative (0 repeats a row), but in outputs row strides are at least D, batch
+ * strides at least (L - 1) row + D (both without meaning where that size is 1).
+ * Outputs may not overlap the inputs, or one another.
+ * State, gates and sums are fp32; y and the gradients dv, df, dg are rounded once.
+ * Sums are taken in a fixed order: results are bit-reproducible.
+ * Supported: B in [1, 2^20], L in [1, 2^24], D a multiple of 8 in [8, 2^16],
+ * B * L * D < 2^40 (and B * D < 2^31).
+ */
+typedef struct {
+  int B, L, D, dtype;           /* dtype of v, f, g, y, dy and their gradients */
+  const void *v, *f, *g;        /* [B][L][D], g may be NULL */
+  long long v_batch, v_row, f_batch, f_row, g_batch, g_row;  /* elements */
+  const float *bias;            /* [D], or NULL: 0 */
+  const float *h0;              /* [B][D], or NULL: 0 */
+  const unsigned char *reset;   /* [B][L], or NULL (any address) */
+  const int *lens;              /* [B], or NULL (4-byte aligned) */
+} hyena_glr_inputs;
+
+/* Scratch of the forward and the backward pass; 0 for unsupported sizes. */
+size_t hyena_glr_workspace_bytes(int B, int L, int D, int dtype);
+size_t hyena_glr_bwd_workspace_bytes(int B, int L, int D, int dtype);
+
+/* y [B][L][D] at the given strides; h_last [B][D] (or NULL): the state after the
+ * last position. */
+int hyena_glr_fwd(const hyena_glr_inputs *in, void *y, long long y_batch, long long y_row, float *h_last,
+                  void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradients of sum(dy * y) + sum(dh_last * h_last), recomputed from the inputs:
+ *   lam_t = dy_t silu(g_t) + a_{t+1} lam_{t+1}   (lam_{L-1} also takes dh_last)
+ *   dv_t = (1 - a_t) lam_t,  df_t = a_t (1 - a_t) lam_t (h_{t-1} - v_t),
+ *   dg_t = dy_t h_t silu'(g_t),  dbias = sum_{b,t} df_t,  dh0 = a_0 lam_0
+ * (h_{t-1} and a_t lam_t are 0 where reset[t] is set).
+ *   dy       [B][L][D] at its strides; dh_last [B][D] or NULL (0)
+ *   dv, df, dg   at the common strides d_batch, d_row (so that they may be column
+ *            blocks of one gradient of the projection); overwritten, zero at padding;
+ *            dg NULL exactly if g is
+ *   dbias [D], dh0 [B][D]   fp32, each may be NULL */
+int hyena_glr_bwd(const hyena_glr_inputs *in, const void *dy, long long dy_batch, long long dy_row,
+                  const float *dh_last, void *dv, void *df, void *dg, long long d_batch, long long d_row,
+                  float *dbias, float *dh0, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* One position of B sequences, their states in a table (decoding).
+ *   v, f, g  [B][D] at row strides v_row, f_row, g_row; g may be NULL; bias as above
+ *   state, state_out  [S][D] fp32; state_out may be state (in place), but they may
+ *            not overlap otherwise
+ *   slots    [B]: row r advances the state of slot slots[r] (4-byte aligned; NULL:
+ *            slot r, S >= B). A row whose slot is outside [0, S) is skipped: its y is
+ *            left as it was. Rows of one slot are consecutive positions of that
+ *            sequence, in row order. Slots that no row names are not written.
+ *   y        [B][D] at y_row
+ * Supported: B in [1, 8192], S in [1, 2^24], D as above. */
+int hyena_glr_step(int B, int D, int S, int dtype, const void *v, long long v_row, const void *f, long long f_row,
+                   const void *g, long long g_row, const float *bias, const int *slots, const float *state,
+                   float *state_out, void *y, long long y_row, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

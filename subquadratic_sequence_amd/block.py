@@ -1,0 +1,190 @@
+"""ctypes binding of the operators around the long convolution in a block: the
+gated linear recurrence (argument marshalling and checks only; the computation
+is in libhyena.so).
+
+Tensors are on one GPU, which need not be the current one; work goes to that
+GPU's current stream, where workspaces are allocated too.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .hyena import GlrInputs, HyenaError, _check, _dtype_code, lib
+
+_vp = ctypes.c_void_p
+
+
+def _p(t):
+    return None if t is None else _vp(t.data_ptr())
+
+
+class _On:
+    """The GPU that holds all the tensors, made current for the call; its stream."""
+
+    def __init__(self, *tensors):
+        ts = [t for t in tensors if t is not None]
+        dev = ts[0].device
+        for t in ts:
+            if t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}")
+        if dev.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, not {dev}")
+        self.device = dev
+        self.guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        self.guard.__enter__()
+        self.stream = _vp(torch.cuda.current_stream(self.device).cuda_stream)
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+    def scratch(self, ws, need, where):
+        if need == 0:
+            raise HyenaError(2, where)
+        if ws is None:
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        if ws.device != self.device:
+            raise ValueError(f"workspace on {ws.device}, tensors on {self.device}")
+        if not ws.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
+        return ws
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def _tensor(t, name, shape, dtype):
+    """A contiguous tensor of this shape and dtype, or None."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name, shape, dtype):
+    """Strides of a tensor with contiguous rows, in elements, without its last
+    dimension (0 for dimensions of size 1)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])]
+
+
+# ------------------------------------------------- gated linear recurrence
+
+
+def hyena_glr_workspace_bytes(B, L, D, dtype) -> int:
+    return lib().hyena_glr_workspace_bytes(B, L, D, dtype)
+
+
+def hyena_glr_bwd_workspace_bytes(B, L, D, dtype) -> int:
+    return lib().hyena_glr_bwd_workspace_bytes(B, L, D, dtype)
+
+
+def _glr_inputs(v, f, g, bias, h0, reset, lens):
+    if not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("v: expected a tensor [B, L, D]")
+    B, L, D = v.shape
+    dt = _dtype_code(v)
+    sv, sf = _rows(v, "v", v.shape, v.dtype), _rows(f, "f", v.shape, v.dtype)
+    sg = [0, 0] if g is None else _rows(g, "g", v.shape, v.dtype)
+    _tensor(bias, "bias", (D,), torch.float32)
+    _tensor(h0, "h0", (B, D), torch.float32)
+    if reset is not None and reset.dtype == torch.bool:
+        reset = reset.view(torch.uint8)
+    _tensor(reset, "reset", (B, L), torch.uint8)
+    _tensor(lens, "lens", (B,), torch.int32)
+    return GlrInputs(B, L, D, dt, _p(v), _p(f), _p(g), *sv, *sf, *sg, _p(bias), _p(h0), _p(reset), _p(lens))
+
+
+def hyena_glr_fwd(v, f, g=None, bias=None, h0=None, reset=None, lens=None, y=None, h_last=None, ws=None):
+    """y_t = h_t silu(g_t) with h_t = a_t h_{t-1} + (1 - a_t) v_t, a = sigmoid(f + bias).
+
+    v, f, g, y [B, L, D] (float32 or bfloat16, contiguous rows: column blocks of one
+    tensor are fine); bias [D], h0 and h_last [B, D] float32; reset [B, L] uint8 or
+    bool; lens [B] int32. The state after the last position goes to h_last, if
+    given. Positions behind lens are left as they are in a given y, zero otherwise."""
+    c = _glr_inputs(v, f, g, bias, h0, reset, lens)
+    if y is not None:
+        sy = _rows(y, "y", v.shape, v.dtype)
+    _tensor(h_last, "h_last", (c.B, c.D), torch.float32)
+    with _On(v, f, g, bias, h0, reset, lens, y, h_last) as on:
+        if y is None:
+            y = (torch.empty if lens is None else torch.zeros)(v.shape, dtype=v.dtype, device=v.device)
+            sy = _rows(y, "y", v.shape, v.dtype)
+        ws = on.scratch(ws, hyena_glr_workspace_bytes(c.B, c.L, c.D, c.dtype), "hyena_glr_workspace_bytes")
+        _check(lib().hyena_glr_fwd(ctypes.byref(c), _p(y), *sy, _p(h_last), _p(ws), _nbytes(ws), on.stream),
+               "hyena_glr_fwd")
+    return y
+
+
+def hyena_glr_bwd(v, f, dy, g=None, bias=None, h0=None, reset=None, lens=None, dh_last=None, dp=None, ws=None):
+    """Gradients of sum(dy * y) + sum(dh_last * h_last) of hyena_glr_fwd: a dict with
+    dv, df (and dg, if g is given; dtype of v), dbias [D] and dh0 [B, D] (float32).
+    dv, df, dg are the column blocks of one tensor dp [B, L, 3D] (2D without g), in
+    the dict too: the gradient of the projection that v, f, g come from."""
+    c = _glr_inputs(v, f, g, bias, h0, reset, lens)
+    B, L, D = v.shape
+    n = 2 if g is None else 3
+    sdy = _rows(dy, "dy", v.shape, v.dtype)
+    _tensor(dh_last, "dh_last", (B, D), torch.float32)
+    _tensor(dp, "dp", (B, L, n * D), v.dtype)
+    with _On(v, f, g, bias, h0, reset, lens, dy, dh_last, dp) as on:
+        if dp is None:
+            dp = torch.empty(B, L, n * D, dtype=v.dtype, device=v.device)
+        out = dict(dp=dp, dv=dp[..., :D], df=dp[..., D:2 * D], dbias=torch.empty(D, device=v.device),
+                   dh0=torch.empty(B, D, device=v.device))
+        if g is not None:
+            out["dg"] = dp[..., 2 * D:]
+        ws = on.scratch(ws, hyena_glr_bwd_workspace_bytes(B, L, D, c.dtype), "hyena_glr_bwd_workspace_bytes")
+        _check(lib().hyena_glr_bwd(ctypes.byref(c), _p(dy), *sdy, _p(dh_last), _p(out["dv"]), _p(out["df"]),
+                                   _p(out.get("dg")), L * n * D, n * D, _p(out["dbias"]), _p(out["dh0"]), _p(ws),
+                                   _nbytes(ws), on.stream), "hyena_glr_bwd")
+    return out
+
+
+def hyena_glr_step(state, v, f, g=None, bias=None, slots=None, state_out=None, y=None):
+    """One position of B sequences: v, f, g, y [B, D]; state [S, D] float32, advanced
+    in place or into state_out. slots [B] int32: the row of state of each sequence
+    (default: row r); rows with a slot outside [0, S) are skipped (zero in a new y),
+    rows that share a slot are consecutive positions of one sequence."""
+    if not isinstance(v, torch.Tensor) or v.dim() != 2:
+        raise ValueError("v: expected a tensor [B, D]")
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise ValueError("state: expected a tensor [S, D]")
+    B, D = v.shape
+    S = state.shape[0]
+    dt = _dtype_code(v)
+    _tensor(state, "state", (S, D), torch.float32)
+    _tensor(state_out, "state_out", (S, D), torch.float32)
+    _tensor(bias, "bias", (D,), torch.float32)
+    _tensor(slots, "slots", (B,), torch.int32)
+    sv, sf = _rows(v, "v", v.shape, v.dtype), _rows(f, "f", v.shape, v.dtype)
+    sg = [0] if g is None else _rows(g, "g", v.shape, v.dtype)
+    if y is not None:
+        sy = _rows(y, "y", v.shape, v.dtype)
+    if state_out is None:
+        state_out = state
+    with _On(v, f, g, bias, slots, state, state_out, y) as on:
+        if y is None:
+            y = (torch.empty if slots is None else torch.zeros)(B, D, dtype=v.dtype, device=v.device)
+            sy = _rows(y, "y", v.shape, v.dtype)
+        _check(lib().hyena_glr_step(B, D, S, dt, _p(v), *sv, _p(f), *sf, _p(g), *sg, _p(bias), _p(slots), _p(state),
+                                    _p(state_out), _p(y), *sy, on.stream), "hyena_glr_step")
+    return y

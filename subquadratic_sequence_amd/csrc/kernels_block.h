@@ -1,0 +1,62 @@
+// Internal launcher interface between the C ABI (block_api.cpp) and the kernels
+// of the operators around the long convolution.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+
+namespace hy {
+
+// ------------------------------------------------ gated linear recurrence
+constexpr int kGlrTile = 64;  // channels per workgroup
+constexpr int kGlrSubs = 16;  // time runs per sub-block (one per 16 lanes of a 256-thread workgroup)
+
+// Split of the sequence: sub-blocks of SB positions, NSB sub-blocks per chunk,
+// C chunks, one workgroup per (channel tile, chunk, sample).
+struct GlrPlan {
+  int R, SB, nsb_total, nsb, C, ctiles;
+};
+GlrPlan glr_plan(int B, int L, int D, bool bf16, bool bwd);
+
+struct GlrArgs {
+  int B, L, D;
+  const void *v, *f, *g;
+  long long vb, vr, fb, fr, gb, gr;
+  const float *bias, *h0;
+  const unsigned char* reset;
+  const int* lens;
+  // forward
+  void* y;
+  long long yb, yr;
+  float* h_last;
+  // backward
+  const void* dy;
+  long long dyb, dyr;
+  const float* dh_last;
+  void *dv, *df, *dg;
+  long long db, dr;
+  float *dbias, *dh0;
+  // workspace: chunk aggregates [B][C][D] (float2 (A, X); backward also R), sub-block
+  // aggregates [B][nsb_total][D] float2 and bias partials [B][C][D] (backward)
+  float2* agg;
+  float* agg_r;
+  float2* sub;
+  float* part;
+};
+hipError_t glr_fwd(const GlrArgs& a, const GlrPlan& p, bool bf16, hipStream_t s);
+hipError_t glr_bwd(const GlrArgs& a, const GlrPlan& p, bool bf16, hipStream_t s);
+
+struct GlrStepArgs {
+  int B, D, S;
+  const void *v, *f, *g;
+  long long vr, fr, gr;
+  const float* bias;
+  const int* slots;
+  const float* state;
+  float* state_out;
+  void* y;
+  long long yr;
+};
+hipError_t glr_step(const GlrStepArgs& a, bool bf16, hipStream_t s);
+
+}  // namespace hy

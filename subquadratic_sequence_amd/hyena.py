@@ -22,6 +22,7 @@ STATUS = {0: "HYENA_OK", 1: "HYENA_ERR_INVALID_ARG", 2: "HYENA_ERR_UNSUPPORTED",
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
 
 
 class FilterParams(ctypes.Structure):
@@ -56,6 +57,12 @@ ND_CIRCULAR = 1
 
 class NDFilmParams(ctypes.Structure):
     _fields_ = [("registers", _i), ("q", _vp), ("film_w", _vp), ("film_b", _vp), ("omega0", _vp)]
+
+
+class GlrInputs(ctypes.Structure):
+    _fields_ = [("B", _i), ("L", _i), ("D", _i), ("dtype", _i), ("v", _vp), ("f", _vp), ("g", _vp),
+                ("v_batch", _ll), ("v_row", _ll), ("f_batch", _ll), ("f_row", _ll), ("g_batch", _ll), ("g_row", _ll),
+                ("bias", _vp), ("h0", _vp), ("reset", _vp), ("lens", _vp)]
 
 
 # name -> (restype, argtypes)
@@ -96,6 +103,12 @@ SIGNATURES = {
     "hyena_nd_film_fwd_profiled": (_i, [_i, _i, _i, _i, _i, _i, ctypes.POINTER(NDFilterParams),
                                         ctypes.POINTER(NDFilmParams), _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp,
                                         _sz, _vp, ctypes.POINTER(_vp)]),
+    "hyena_glr_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "hyena_glr_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "hyena_glr_fwd": (_i, [ctypes.POINTER(GlrInputs), _vp, _ll, _ll, _vp, _vp, _sz, _vp]),
+    "hyena_glr_bwd": (_i, [ctypes.POINTER(GlrInputs), _vp, _ll, _ll, _vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _vp,
+                           _sz, _vp]),
+    "hyena_glr_step": (_i, [_i, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _vp, _ll, _vp]),
 }
 
 _lib = None
