@@ -435,6 +435,43 @@ int hyena_glr_step(int B, int D, int S, int dtype, const void *v, long long v_ro
                    const void *g, long long g_row, const float *bias, const int *slots, const float *state,
                    float *state_out, void *y, long long y_row, hipStream_t stream);
 
+/* ------------------------------------------- group norm, channels last ---- */
+/* Activations of the gated feed-forward block and of the group norm. */
+typedef enum { HYENA_ACT_NONE = 0, HYENA_ACT_SILU = 1, HYENA_ACT_GELU = 2 /* x Phi(x), the erf form */ } hyena_act;
+
+/*
+ * x [B][S][C] (a grid [B][X][Y][Z][C] has S = X Y Z; S = 1 normalises every row by
+ * itself). The channels form G groups of C / G neighbours; over the S positions and
+ * the channels of a group, per sample:
+ *   mean, var = E[(x - mean)^2],  rstd = 1 / sqrt(var + eps)
+ *   n = gamma (x - mean) rstd + beta,  y = act(n)
+ * Positions s >= lens[b] (clamped to [0, S]) are padding: they enter no statistic,
+ * whatever they hold, y is left as it was there and dx is 0. A sample with lens[b] = 0
+ * has mean 0 and rstd 1 / sqrt(eps).
+ * Statistics and sums are fp32 in a fixed order (bit-reproducible), the variance from
+ * deviations, not from the difference of two large sums.
+ * Supported: B in [1, 2^24], S in [1, 2^24], C a multiple of 8 in [8, 8192], G a
+ * divisor of C, eps > 0 and finite, B * S * C < 2^40 and B * C < 2^31.
+ */
+size_t hyena_group_norm_workspace_bytes(int B, int S, int C, int G, int dtype);
+size_t hyena_group_norm_bwd_workspace_bytes(int B, int S, int C, int G, int dtype);
+
+/*   x, y [B][S][C] dtype (y may be x: in place); gamma, beta [C] fp32 or NULL (1, 0)
+ *   lens [B] or NULL (4-byte aligned); mean, rstd [B][G] fp32 (outputs; both may be NULL) */
+int hyena_group_norm_fwd(int B, int S, int C, int G, int dtype, int act, float eps, const void *x,
+                         const float *gamma, const float *beta, const int *lens, void *y, float *mean,
+                         float *rstd, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* With dn = dy act'(n) and xh = (x - mean) rstd, the sums over a sample's group
+ * m1 = avg(gamma dn), m2 = avg(gamma dn xh):
+ *   dx = rstd (gamma dn - m1 - xh m2),  dgamma = sum_{b,s} dn xh,  dbeta = sum_{b,s} dn
+ *   mean, rstd   [B][G] as the forward wrote them; dy, dx [B][S][C] dtype (dx may be dy)
+ *   dgamma, dbeta   [C] fp32, each may be NULL */
+int hyena_group_norm_bwd(int B, int S, int C, int G, int dtype, int act, const void *x, const void *dy,
+                         const float *gamma, const float *beta, const int *lens, const float *mean,
+                         const float *rstd, void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                         hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

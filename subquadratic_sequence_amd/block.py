@@ -1,5 +1,5 @@
 """ctypes binding of the operators around the long convolution in a block: the
-gated linear recurrence (argument marshalling and checks only; the computation
+gated linear recurrence and the group norm (argument marshalling and checks only; the computation
 is in libhyena.so).
 
 Tensors are on one GPU, which need not be the current one; work goes to that
@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from .hyena import GlrInputs, HyenaError, _check, _dtype_code, lib
+from .hyena import ACT_NONE, GlrInputs, HyenaError, _check, _dtype_code, lib
 
 _vp = ctypes.c_void_p
 
@@ -188,3 +188,76 @@ def hyena_glr_step(state, v, f, g=None, bias=None, slots=None, state_out=None, y
         _check(lib().hyena_glr_step(B, D, S, dt, _p(v), *sv, _p(f), *sf, _p(g), *sg, _p(bias), _p(slots), _p(state),
                                     _p(state_out), _p(y), *sy, on.stream), "hyena_glr_step")
     return y
+
+
+# ------------------------------------------------ group norm, channels last
+
+
+def hyena_group_norm_workspace_bytes(B, S, C, G, dtype) -> int:
+    return lib().hyena_group_norm_workspace_bytes(B, S, C, G, dtype)
+
+
+def hyena_group_norm_bwd_workspace_bytes(B, S, C, G, dtype) -> int:
+    return lib().hyena_group_norm_bwd_workspace_bytes(B, S, C, G, dtype)
+
+
+def _norm_shape(x):
+    """(B, S, C) of x [B, ..., C]; two dimensions are rows by themselves (S = 1)."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x: expected a tensor [B, ..., C]")
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    return x.shape[0], S, x.shape[-1]
+
+
+def hyena_group_norm_fwd(x, groups, gamma=None, beta=None, eps=1e-5, act=ACT_NONE, lens=None, y=None, mean=None,
+                         rstd=None, ws=None):
+    """y = act(gamma (x - mean) rstd + beta) for x [B, ..., C] (channels last; float32 or
+    bfloat16), mean and rstd over the positions of a sample and the C / groups
+    channels of a group. gamma, beta [C] float32; lens [B] int32: positions in use;
+    mean, rstd [B, groups] float32 receive the statistics (the backward takes them).
+    y may be x. Positions behind lens are left as they are in a given y, zero otherwise."""
+    B, S, C = _norm_shape(x)
+    dt = _dtype_code(x)
+    _tensor(x, "x", x.shape, x.dtype)
+    _tensor(gamma, "gamma", (C,), torch.float32)
+    _tensor(beta, "beta", (C,), torch.float32)
+    _tensor(lens, "lens", (B,), torch.int32)
+    _tensor(y, "y", x.shape, x.dtype)
+    _tensor(mean, "mean", (B, groups), torch.float32)
+    _tensor(rstd, "rstd", (B, groups), torch.float32)
+    with _On(x, gamma, beta, lens, y, mean, rstd) as on:
+        if y is None:
+            y = (torch.empty_like if lens is None else torch.zeros_like)(x)
+        ws = on.scratch(ws, hyena_group_norm_workspace_bytes(B, S, C, groups, dt), "hyena_group_norm_workspace_bytes")
+        _check(lib().hyena_group_norm_fwd(B, S, C, groups, dt, act, eps, _p(x), _p(gamma), _p(beta), _p(lens), _p(y),
+                                          _p(mean), _p(rstd), _p(ws), _nbytes(ws), on.stream), "hyena_group_norm_fwd")
+    return y
+
+
+def hyena_group_norm_bwd(x, dy, groups, mean, rstd, gamma=None, beta=None, act=ACT_NONE, lens=None, dx=None, ws=None):
+    """Gradients of sum(dy * y), y = hyena_group_norm_fwd(x, ...), mean and rstd as it
+    wrote them: a dict with dx (dtype of x, zero behind lens; dx may be dy) and
+    dgamma, dbeta [C] float32 (also where gamma or beta were left out)."""
+    B, S, C = _norm_shape(x)
+    dt = _dtype_code(x)
+    _tensor(x, "x", x.shape, x.dtype)
+    _tensor(dy, "dy", x.shape, x.dtype)
+    _tensor(gamma, "gamma", (C,), torch.float32)
+    _tensor(beta, "beta", (C,), torch.float32)
+    _tensor(lens, "lens", (B,), torch.int32)
+    _tensor(dx, "dx", x.shape, x.dtype)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is None:
+            raise ValueError(f"{name}: the forward's statistics are needed")
+        _tensor(t, name, (B, groups), torch.float32)
+    with _On(x, dy, gamma, beta, lens, mean, rstd, dx) as on:
+        out = dict(dx=torch.empty_like(x) if dx is None else dx, dgamma=torch.empty(C, device=x.device),
+                   dbeta=torch.empty(C, device=x.device))
+        ws = on.scratch(ws, hyena_group_norm_bwd_workspace_bytes(B, S, C, groups, dt),
+                        "hyena_group_norm_bwd_workspace_bytes")
+        _check(lib().hyena_group_norm_bwd(B, S, C, groups, dt, act, _p(x), _p(dy), _p(gamma), _p(beta), _p(lens),
+                                          _p(mean), _p(rstd), _p(out["dx"]), _p(out["dgamma"]), _p(out["dbeta"]),
+                                          _p(ws), _nbytes(ws), on.stream), "hyena_group_norm_bwd")
+    return out

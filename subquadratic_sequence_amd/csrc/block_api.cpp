@@ -109,6 +109,31 @@ hy::GlrArgs glr_args(const hyena_glr_inputs* in) {
   return a;
 }
 
+// ------------------------------------------------ group norm, channels last
+bool act_ok(int act) { return act == HYENA_ACT_NONE || act == HYENA_ACT_SILU || act == HYENA_ACT_GELU; }
+
+bool gn_shape_ok(int B, int S, int C, int G) {
+  if (B < 1 || B > (1 << 24) || S < 1 || S > (1 << 24) || C < 8 || C > 8192 || C % 8) return false;
+  if (G < 1 || G > C || C % G) return false;
+  if ((long long)B * C >= (1LL << 31)) return false;
+  return (long long)B * C <= (kMaxElems - 1) / S;
+}
+
+struct GnWs {
+  size_t part, chan, total;
+};
+GnWs gn_ws(int B, int S, int C, int G, bool bwd) {
+  const hy::GnPlan p = hy::gn_plan(B, S, C, G);
+  GnWs w{};
+  size_t off = 0;
+  w.part = off;
+  if (p.chunks > 1) off = align_up(off + (size_t)B * p.chunks * G * 8, kAlign);
+  w.chan = off;
+  if (bwd) off = align_up(off + (size_t)p.chan_rows * 2 * C * 4, kAlign);
+  w.total = off ? off : kAlign;
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -193,6 +218,84 @@ int hyena_glr_step(int B, int D, int S, int dtype, const void* v, long long v_ro
   if (device_ok() != HYENA_OK) return HYENA_ERR_HIP;
   hy::GlrStepArgs a{B, D, S, v, f, g, v_row, f_row, g_row, bias, slots, state, state_out, y, y_row};
   HY_CHECK_HIP(hy::glr_step(a, dtype == HYENA_BF16, stream));
+  return HYENA_OK;
+}
+
+size_t hyena_group_norm_workspace_bytes(int B, int S, int C, int G, int dtype) {
+  if (!gn_shape_ok(B, S, C, G) || !dtype_ok(dtype)) return 0;
+  return gn_ws(B, S, C, G, false).total;
+}
+
+size_t hyena_group_norm_bwd_workspace_bytes(int B, int S, int C, int G, int dtype) {
+  if (!gn_shape_ok(B, S, C, G) || !dtype_ok(dtype)) return 0;
+  return gn_ws(B, S, C, G, true).total;
+}
+
+int hyena_group_norm_fwd(int B, int S, int C, int G, int dtype, int act, float eps, const void* x, const float* gamma,
+                         const float* beta, const int* lens, void* y, float* mean, float* rstd, void* ws,
+                         size_t ws_bytes, hipStream_t stream) {
+  if (!dtype_ok(dtype) || !act_ok(act) || B < 1) return HYENA_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || !isfinite(eps)) return HYENA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(ws)) return HYENA_ERR_INVALID_ARG;
+  if (!aligned16_or_null(gamma) || !aligned16_or_null(beta) || !aligned16_or_null(mean) || !aligned16_or_null(rstd) ||
+      !aligned(lens, 4))
+    return HYENA_ERR_INVALID_ARG;
+  if (!gn_shape_ok(B, S, C, G)) return HYENA_ERR_UNSUPPORTED;
+  const GnWs w = gn_ws(B, S, C, G, false);
+  if (ws_bytes < w.total) return HYENA_ERR_WORKSPACE;
+  if (device_ok() != HYENA_OK) return HYENA_ERR_HIP;
+  hy::GnArgs a{};
+  a.B = B;
+  a.S = S;
+  a.C = C;
+  a.G = G;
+  a.act = act;
+  a.eps = eps;
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.lens = lens;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.part = reinterpret_cast<float2*>(static_cast<char*>(ws) + w.part);
+  HY_CHECK_HIP(hy::gn_fwd(a, hy::gn_plan(B, S, C, G), dtype == HYENA_BF16, stream));
+  return HYENA_OK;
+}
+
+int hyena_group_norm_bwd(int B, int S, int C, int G, int dtype, int act, const void* x, const void* dy,
+                         const float* gamma, const float* beta, const int* lens, const float* mean, const float* rstd,
+                         void* dx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!dtype_ok(dtype) || !act_ok(act) || B < 1) return HYENA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(dy) || !aligned16(dx) || !aligned16(mean) || !aligned16(rstd) || !aligned16(ws))
+    return HYENA_ERR_INVALID_ARG;
+  if (!aligned16_or_null(gamma) || !aligned16_or_null(beta) || !aligned16_or_null(dgamma) ||
+      !aligned16_or_null(dbeta) || !aligned(lens, 4))
+    return HYENA_ERR_INVALID_ARG;
+  if (!gn_shape_ok(B, S, C, G)) return HYENA_ERR_UNSUPPORTED;
+  const GnWs w = gn_ws(B, S, C, G, true);
+  if (ws_bytes < w.total) return HYENA_ERR_WORKSPACE;
+  if (device_ok() != HYENA_OK) return HYENA_ERR_HIP;
+  char* wb = static_cast<char*>(ws);
+  hy::GnArgs a{};
+  a.B = B;
+  a.S = S;
+  a.C = C;
+  a.G = G;
+  a.act = act;
+  a.x = x;
+  a.dy = dy;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.lens = lens;
+  a.dx = dx;
+  a.mean_in = mean;
+  a.rstd_in = rstd;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.part = reinterpret_cast<float2*>(wb + w.part);
+  a.chan = reinterpret_cast<float*>(wb + w.chan);
+  HY_CHECK_HIP(hy::gn_bwd(a, hy::gn_plan(B, S, C, G), dtype == HYENA_BF16, stream));
   return HYENA_OK;
 }
 

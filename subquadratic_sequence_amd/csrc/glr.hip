@@ -17,7 +17,7 @@
 // (A, X[, R]) of each chunk, and every workgroup of the second folds those of
 // the chunks before it (behind it for mu) in order: no waiting between
 // workgroups and no order that varies.
-#include "common.h"
+#include "act.h"
 #include "kernels_block.h"
 
 namespace hy {
@@ -48,38 +48,6 @@ __device__ __forceinline__ void store4(bf16* p, const float (&v)[4]) {
   *reinterpret_cast<bf16v4*>(p) = r;
 }
 __device__ __forceinline__ void load4f(const float* p, float (&v)[4]) { unpack(*reinterpret_cast<const float4*>(p), v); }
-
-// sigmoid(z) and 1 - sigmoid(z) = sigmoid(-z), both to a relative error of a few
-// 2^-24: e = exp(-|z|) through the hardware exp2 of a product split in two words
-// (the rounding error of |z| log2(e) is put back as a factor), one Newton step
-// on the hardware reciprocal.
-__device__ __forceinline__ void sigmoids(float z, float& s, float& c) {
-  const float L2E = 1.44269504088896341f, L2E_LO = 1.92596299e-8f, LN2 = 0.693147180559945309f;
-  const float x = -fabsf(z);
-  const float hi = x * L2E;
-  const float lo = fmaf(x, L2E_LO, fmaf(x, L2E, -hi));
-  float e = __builtin_amdgcn_exp2f(hi);
-  e = x < -200.f ? 0.f : fmaf(e, lo * LN2, e);  // below exp(-200) = 0 in fp32 (and lo of -inf is NaN)
-  const float d = 1.f + e;
-  float r = __builtin_amdgcn_rcpf(d);
-  r = fmaf(r, fmaf(-d, r, 1.f), r);
-  const float q = e * r;
-  s = z >= 0.f ? r : q;
-  c = z >= 0.f ? q : r;
-}
-// silu(g) and silu'(g) = s (1 + g (1 - s))
-__device__ __forceinline__ float silu_f(float g) {
-  float s, c;
-  sigmoids(g, s, c);
-  return g < -200.f ? 0.f : g * s;  // -inf * 0
-}
-__device__ __forceinline__ void silu_d(float g, float& y, float& d) {
-  float s, c;
-  sigmoids(g, s, c);
-  const bool tail = fabsf(g) > 200.f;  // infinities: s c g is 0 there
-  y = g < -200.f ? 0.f : g * s;
-  d = tail ? s : fmaf(g * s, c, s);
-}
 
 // A h + X for a run; A = 0 (a reset inside the run) cuts off whatever h holds
 __device__ __forceinline__ float act_on(float A, float h, float X) { return A == 0.f ? X : fmaf(A, h, X); }
@@ -505,27 +473,6 @@ __global__ __launch_bounds__(256) void glr_bwd_kernel(GlrArgs a, GlrPlan p) {
   }
 }
 
-// out[d] = sum over rows of part [rows][D]: 64 channels per workgroup, the rows
-// dealt to 16 threads per channel, their sums joined in order
-__global__ __launch_bounds__(1024) void glr_colsum_kernel(const float* __restrict__ part, float* __restrict__ out,
-                                                          long long rows, int D) {
-  __shared__ float sm[16][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
-  float t = 0.f;
-  if (c < D) {
-#pragma unroll 4
-    for (long long r = q; r < rows; r += 16) t += part[r * D + c];
-  }
-  sm[q][threadIdx.x & 63] = t;
-  __syncthreads();
-  if (q == 0 && c < D) {
-    t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t += sm[i][threadIdx.x];
-    out[c] = t;
-  }
-}
-
 // ------------------------------------------------------------ one position
 // Rows that share a slot are consecutive positions of one sequence: the
 // workgroup of the first such row walks the later ones in row order (the
@@ -594,8 +541,9 @@ hipError_t bwd_go(const GlrArgs& a, const GlrPlan& p, hipStream_t s) {
   const unsigned grid = (unsigned)((long long)p.ctiles * p.C * a.B);
   if (p.nsb_total > 1) glr_agg_kernel<T, R, true, GATE, MASK><<<grid, 256, 0, s>>>(a, p);
   glr_bwd_kernel<T, R, GATE, MASK><<<grid, 256, 0, s>>>(a, p);
-  if (a.dbias) glr_colsum_kernel<<<(a.D + 63) / 64, 1024, 0, s>>>(a.part, a.dbias, (long long)a.B * p.C, a.D);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.dbias) return e;
+  return colsum(a.part, a.dbias, (long long)a.B * p.C, a.D, a.D, s);
 }
 
 }  // namespace

@@ -59,4 +59,37 @@ struct GlrStepArgs {
 };
 hipError_t glr_step(const GlrStepArgs& a, bool bf16, hipStream_t s);
 
+// ------------------------------------------------ group norm, channels last
+struct GnArgs {
+  int B, S, C, G, act;
+  float eps;
+  const void *x, *dy;
+  const float *gamma, *beta;
+  const int* lens;
+  void *y, *dx;
+  float *mean, *rstd;           // forward outputs (may be null)
+  const float *mean_in, *rstd_in;  // backward inputs
+  float *dgamma, *dbeta;        // may be null
+  float2* part;                 // [B][chunks][G]: (mean, M2) or the two group sums
+  float* chan;                  // [rows][2][C] channel sums (backward; both gradients wanted or not)
+};
+// How the rows of a sample are dealt out.
+//   rows form (S = 1, C / G a multiple of 8): `lanes` lanes of `nv` vectors of 8
+//   channels per group, `slots` samples side by side, `per` samples per workgroup;
+//   otherwise `slots` rows of C / 8 threads, chunks of `per` rows
+struct GnPlan {
+  bool rows_form;
+  int threads, slots, per, chunks;
+  int lanes, nv;         // rows form
+  int group_lanes;       // lanes that reduce one group (general form)
+  int samples;           // samples a workgroup of the one-chunk backward takes
+  long long chan_rows;   // rows of the channel sums
+};
+GnPlan gn_plan(int B, int S, int C, int G);
+hipError_t gn_fwd(const GnArgs& a, const GnPlan& p, bool bf16, hipStream_t s);
+hipError_t gn_bwd(const GnArgs& a, const GnPlan& p, bool bf16, hipStream_t s);
+
+// out[d] = sum over rows of part [rows][ld], columns [0, D), in a fixed order
+hipError_t colsum(const float* part, float* out, long long rows, int ld, int D, hipStream_t s);
+
 }  // namespace hy

@@ -50,6 +50,11 @@ class NDLayer(ctypes.Structure):
                 ("cache_bytes", _sz), ("boundary", _i)]
 
 
+# hyena_act
+ACT_NONE = 0
+ACT_SILU = 1
+ACT_GELU = 2
+
 # hyena_nd_boundary
 ND_ZERO_PAD = 0
 ND_CIRCULAR = 1
@@ -108,6 +113,12 @@ SIGNATURES = {
     "hyena_glr_fwd": (_i, [ctypes.POINTER(GlrInputs), _vp, _ll, _ll, _vp, _vp, _sz, _vp]),
     "hyena_glr_bwd": (_i, [ctypes.POINTER(GlrInputs), _vp, _ll, _ll, _vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _vp,
                            _sz, _vp]),
+    "hyena_group_norm_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "hyena_group_norm_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "hyena_group_norm_fwd": (_i, [_i, _i, _i, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _sz, _vp]),
+    "hyena_group_norm_bwd": (_i, [_i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _sz, _vp]),
     "hyena_glr_step": (_i, [_i, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _vp, _ll, _vp]),
 }
 

@@ -26,3 +26,30 @@ def glr(v, f, g=None, bias=None, h0=None, reset=None, lens=None):
         h = new
         ys.append(y)
     return torch.stack(ys, 1), h
+
+
+def act(q, name):
+    if name == "silu":
+        return q * torch.sigmoid(q)
+    if name == "gelu":
+        return 0.5 * q * torch.special.erfc(-q / 2 ** 0.5)
+    return q
+
+
+def group_norm(x, G, gamma=None, beta=None, eps=1e-5, name="none", lens=None):
+    """(y, mean, rstd) of x [B, S, C], sample by sample; y is 0 behind lens."""
+    B, S, C = x.shape
+    ys, means, rstds = [], [], []
+    for b in range(B):
+        n = S if lens is None else min(max(int(lens[b]), 0), S)
+        xb = x[b, :n].reshape(n, G, C // G)
+        mean = xb.mean((0, 2)) if n else x.new_zeros(G)
+        var = (xb - mean[:, None]).square().mean((0, 2)) if n else x.new_zeros(G)
+        rstd = 1 / torch.sqrt(var + eps)
+        h = ((xb - mean[:, None]) * rstd[:, None]).reshape(n, C)
+        h = h if gamma is None else h * gamma
+        h = h if beta is None else h + beta
+        ys.append(torch.cat([act(h, name), x.new_zeros(S - n, C)]))
+        means.append(mean)
+        rstds.append(rstd)
+    return torch.stack(ys), torch.stack(means), torch.stack(rstds)
