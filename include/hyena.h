@@ -435,10 +435,36 @@ int hyena_glr_step(int B, int D, int S, int dtype, const void *v, long long v_ro
                    const void *g, long long g_row, const float *bias, const int *slots, const float *state,
                    float *state_out, void *y, long long y_row, hipStream_t stream);
 
-/* ------------------------------------------- group norm, channels last ---- */
+/* ------------------------------------------ gated feed-forward block ---- */
 /* Activations of the gated feed-forward block and of the group norm. */
 typedef enum { HYENA_ACT_NONE = 0, HYENA_ACT_SILU = 1, HYENA_ACT_GELU = 2 /* x Phi(x), the erf form */ } hyena_act;
 
+/*
+ * The channel mixer of a block, per position (row) x of D channels:
+ *   (p, q) = x W_in,  z = p * act(q),  y = z W_out
+ *   x [M][D], w_in [D][2F] (column blocks: p, then q), w_out [F][D], y [M][D], all dtype
+ * Both projections of W_in, the activation and the product run in one kernel (p and
+ * q stay in registers); z is kept in the storage type between the two products.
+ * Backward, p and q recomputed from x:
+ *   dz = dy W_out^T, dp = dz act(q), dq = dz p act'(q)      (one kernel)
+ *   dx = [dp dq] W_in^T,  dw_in = x^T [dp dq],  dw_out = z^T dy
+ * with z, dp and dq in the storage type, and every sum over K, rows included, in
+ * fp32. The gradients have the storage type of what they belong to.
+ * Row-major and contiguous. Supported: M in [1, 2^24], D and F multiples of 8 in
+ * [8, 2^16]. y (and the gradients) may not overlap the inputs.
+ */
+size_t hyena_ffn_workspace_bytes(int M, int D, int F, int dtype);
+size_t hyena_ffn_bwd_workspace_bytes(int M, int D, int F, int dtype);
+
+int hyena_ffn_fwd(int M, int D, int F, int dtype, int act, const void *x, const void *w_in, const void *w_out,
+                  void *y, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* dy [M][D] -> dx [M][D], dw_in [D][2F], dw_out [F][D] (dtype, overwritten). */
+int hyena_ffn_bwd(int M, int D, int F, int dtype, int act, const void *x, const void *w_in, const void *w_out,
+                  const void *dy, void *dx, void *dw_in, void *dw_out, void *ws, size_t ws_bytes,
+                  hipStream_t stream);
+
+/* ------------------------------------------- group norm, channels last ---- */
 /*
  * x [B][S][C] (a grid [B][X][Y][Z][C] has S = X Y Z; S = 1 normalises every row by
  * itself). The channels form G groups of C / G neighbours; over the S positions and

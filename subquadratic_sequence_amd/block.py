@@ -1,5 +1,5 @@
 """ctypes binding of the operators around the long convolution in a block: the
-gated linear recurrence and the group norm (argument marshalling and checks only; the computation
+gated linear recurrence, the gated feed-forward block and the group norm (argument marshalling and checks only; the computation
 is in libhyena.so).
 
 Tensors are on one GPU, which need not be the current one; work goes to that
@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from .hyena import ACT_NONE, GlrInputs, HyenaError, _check, _dtype_code, lib
+from .hyena import ACT_NONE, ACT_SILU, GlrInputs, HyenaError, _check, _dtype_code, lib
 
 _vp = ctypes.c_void_p
 
@@ -188,6 +188,66 @@ def hyena_glr_step(state, v, f, g=None, bias=None, slots=None, state_out=None, y
         _check(lib().hyena_glr_step(B, D, S, dt, _p(v), *sv, _p(f), *sf, _p(g), *sg, _p(bias), _p(slots), _p(state),
                                     _p(state_out), _p(y), *sy, on.stream), "hyena_glr_step")
     return y
+
+
+# ---------------------------------------------- gated feed-forward block
+
+
+def hyena_ffn_workspace_bytes(M, D, F, dtype) -> int:
+    return lib().hyena_ffn_workspace_bytes(M, D, F, dtype)
+
+
+def hyena_ffn_bwd_workspace_bytes(M, D, F, dtype) -> int:
+    return lib().hyena_ffn_bwd_workspace_bytes(M, D, F, dtype)
+
+
+def _ffn_shape(x, w_in, w_out):
+    """(M, D, F) of x [..., D]: its leading dimensions are M rows."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x: expected a tensor [..., D]")
+    if not isinstance(w_out, torch.Tensor) or w_out.dim() != 2:
+        raise ValueError("w_out: expected a tensor [F, D]")
+    D, F = x.shape[-1], w_out.shape[0]
+    M = 1
+    for n in x.shape[:-1]:
+        M *= n
+    _tensor(x, "x", x.shape, x.dtype)
+    _tensor(w_out, "w_out", (F, D), x.dtype)
+    if w_in is None:
+        raise TypeError("w_in: expected a torch tensor")
+    _tensor(w_in, "w_in", (D, 2 * F), x.dtype)
+    return M, D, F
+
+
+def hyena_ffn_fwd(x, w_in, w_out, act=ACT_SILU, y=None, ws=None):
+    """y = (p * act(q)) w_out with (p, q) = x w_in: x, y [..., D], w_in [D, 2F] (the
+    columns of p, then those of q), w_out [F, D], all float32 or bfloat16."""
+    M, D, F = _ffn_shape(x, w_in, w_out)
+    dt = _dtype_code(x)
+    _tensor(y, "y", x.shape, x.dtype)
+    with _On(x, w_in, w_out, y) as on:
+        if y is None:
+            y = torch.empty_like(x)
+        ws = on.scratch(ws, hyena_ffn_workspace_bytes(M, D, F, dt), "hyena_ffn_workspace_bytes")
+        _check(lib().hyena_ffn_fwd(M, D, F, dt, act, _p(x), _p(w_in), _p(w_out), _p(y), _p(ws), _nbytes(ws),
+                                   on.stream), "hyena_ffn_fwd")
+    return y
+
+
+def hyena_ffn_bwd(x, w_in, w_out, dy, act=ACT_SILU, ws=None):
+    """Gradients of sum(dy * y), y = hyena_ffn_fwd(x, w_in, w_out, act): a dict with dx,
+    dw_in, dw_out (shapes and dtype of x, w_in, w_out)."""
+    M, D, F = _ffn_shape(x, w_in, w_out)
+    dt = _dtype_code(x)
+    if dy is None:
+        raise TypeError("dy: expected a torch tensor")
+    _tensor(dy, "dy", x.shape, x.dtype)
+    with _On(x, w_in, w_out, dy) as on:
+        g = dict(dx=torch.empty_like(x), dw_in=torch.empty_like(w_in), dw_out=torch.empty_like(w_out))
+        ws = on.scratch(ws, hyena_ffn_bwd_workspace_bytes(M, D, F, dt), "hyena_ffn_bwd_workspace_bytes")
+        _check(lib().hyena_ffn_bwd(M, D, F, dt, act, _p(x), _p(w_in), _p(w_out), _p(dy), _p(g["dx"]), _p(g["dw_in"]),
+                                   _p(g["dw_out"]), _p(ws), _nbytes(ws), on.stream), "hyena_ffn_bwd")
+    return g
 
 
 # ------------------------------------------------ group norm, channels last

@@ -134,6 +134,28 @@ GnWs gn_ws(int B, int S, int C, int G, bool bwd) {
   return w;
 }
 
+// ---------------------------------------------- gated feed-forward block
+bool ffn_shape_ok(int M, int D, int F) {
+  if (M < 1 || M > (1 << 24)) return false;
+  return D >= 8 && D <= (1 << 16) && D % 8 == 0 && F >= 8 && F <= (1 << 16) && F % 8 == 0;
+}
+
+struct FfnWs {
+  size_t z, dpq, part, total;
+};
+FfnWs ffn_ws(int M, int D, int F, int dtype, bool bwd) {
+  const hy::FfnPlan p = hy::ffn_plan(M, D, F, dtype == HYENA_BF16, bwd);
+  const size_t e = esize(dtype);
+  FfnWs w{};
+  size_t off = align_up((size_t)M * F * e, kAlign);
+  w.dpq = off;
+  if (bwd) off = align_up(off + (size_t)M * 2 * F * e, kAlign);
+  w.part = off;
+  off = align_up(off + p.part_floats * 4, kAlign);
+  w.total = off;
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -296,6 +318,73 @@ int hyena_group_norm_bwd(int B, int S, int C, int G, int dtype, int act, const v
   a.part = reinterpret_cast<float2*>(wb + w.part);
   a.chan = reinterpret_cast<float*>(wb + w.chan);
   HY_CHECK_HIP(hy::gn_bwd(a, hy::gn_plan(B, S, C, G), dtype == HYENA_BF16, stream));
+  return HYENA_OK;
+}
+
+size_t hyena_ffn_workspace_bytes(int M, int D, int F, int dtype) {
+  if (!ffn_shape_ok(M, D, F) || !dtype_ok(dtype)) return 0;
+  return ffn_ws(M, D, F, dtype, false).total;
+}
+
+size_t hyena_ffn_bwd_workspace_bytes(int M, int D, int F, int dtype) {
+  if (!ffn_shape_ok(M, D, F) || !dtype_ok(dtype)) return 0;
+  return ffn_ws(M, D, F, dtype, true).total;
+}
+
+int hyena_ffn_fwd(int M, int D, int F, int dtype, int act, const void* x, const void* w_in, const void* w_out, void* y,
+                  void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!dtype_ok(dtype) || !act_ok(act) || M < 1) return HYENA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_in) || !aligned16(w_out) || !aligned16(y) || !aligned16(ws))
+    return HYENA_ERR_INVALID_ARG;
+  if (!ffn_shape_ok(M, D, F)) return HYENA_ERR_UNSUPPORTED;
+  const FfnWs w = ffn_ws(M, D, F, dtype, false);
+  if (ws_bytes < w.total) return HYENA_ERR_WORKSPACE;
+  if (device_ok() != HYENA_OK) return HYENA_ERR_HIP;
+  const bool bf = dtype == HYENA_BF16;
+  char* wb = static_cast<char*>(ws);
+  hy::FfnArgs a{};
+  a.M = M;
+  a.D = D;
+  a.F = F;
+  a.act = act;
+  a.x = x;
+  a.w_in = w_in;
+  a.w_out = w_out;
+  a.y = y;
+  a.z = wb + w.z;
+  a.part = reinterpret_cast<float*>(wb + w.part);
+  HY_CHECK_HIP(hy::ffn_fwd(a, hy::ffn_plan(M, D, F, bf, false), bf, stream));
+  return HYENA_OK;
+}
+
+int hyena_ffn_bwd(int M, int D, int F, int dtype, int act, const void* x, const void* w_in, const void* w_out,
+                  const void* dy, void* dx, void* dw_in, void* dw_out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!dtype_ok(dtype) || !act_ok(act) || M < 1) return HYENA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_in) || !aligned16(w_out) || !aligned16(dy) || !aligned16(dx) ||
+      !aligned16(dw_in) || !aligned16(dw_out) || !aligned16(ws))
+    return HYENA_ERR_INVALID_ARG;
+  if (!ffn_shape_ok(M, D, F)) return HYENA_ERR_UNSUPPORTED;
+  const FfnWs w = ffn_ws(M, D, F, dtype, true);
+  if (ws_bytes < w.total) return HYENA_ERR_WORKSPACE;
+  if (device_ok() != HYENA_OK) return HYENA_ERR_HIP;
+  const bool bf = dtype == HYENA_BF16;
+  char* wb = static_cast<char*>(ws);
+  hy::FfnArgs a{};
+  a.M = M;
+  a.D = D;
+  a.F = F;
+  a.act = act;
+  a.x = x;
+  a.w_in = w_in;
+  a.w_out = w_out;
+  a.dy = dy;
+  a.dx = dx;
+  a.dw_in = dw_in;
+  a.dw_out = dw_out;
+  a.z = wb + w.z;
+  a.dpq = wb + w.dpq;
+  a.part = reinterpret_cast<float*>(wb + w.part);
+  HY_CHECK_HIP(hy::ffn_bwd(a, hy::ffn_plan(M, D, F, bf, true), bf, stream));
   return HYENA_OK;
 }
 

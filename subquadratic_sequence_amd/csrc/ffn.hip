@@ -1,0 +1,456 @@
+// Gated feed-forward block: (p, q) = x W_in, z = p act(q), y = z W_out, and its
+// backward pass, on the MFMA units of gfx950.
+//
+// Every product is C [M][N] = A [M][K] B [K][N] in fp32 accumulators, with the
+// operands read as they are stored: K contiguous (rows of x, dy, z; W_in and
+// W_out where their transposes are needed) or K strided (W_in and W_out as they
+// are; both operands of the weight gradients, whose K runs over the rows of x).
+//  * Global to LDS: 16-byte loads that write LDS directly, two tiles in turn, one
+//    barrier per tile: tile t + 1 is on its way while tile t is multiplied.
+//  * LDS: a tile is R rows (or columns) by 128 bytes of K. K contiguous: rows of
+//    128 bytes, 16-byte chunk c of row r at slot c ^ (r & 7), so that the 16 rows
+//    of a fragment read spread over the banks. K strided: rows of k, R elements
+//    each; blocks of 16 columns are exchanged by a function of k so that the rows
+//    of one transposing read (ds_read_b64_tr_b16; for fp32 four 4-byte reads) lie
+//    in different banks.
+//  * MFMA: 16x16x32 bf16 or 4 x 16x16x4 fp32 per fragment pair. The operands go in
+//    swapped, so that a lane ends with four neighbouring columns of one row of C.
+//  * The gated product reads the p and the q columns of W_in as one tile and
+//    multiplies p by act(q) in registers. The backward's first kernel holds p, q
+//    and dz = dy W_out^T for the same rows and columns, so none of them is stored.
+#include <type_traits>
+
+#include "act.h"
+#include "kernels_block.h"
+
+namespace hy {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+
+constexpr int kThreads = 512;         // 8 waves
+constexpr int kWm = 2, kWn = 4;       // wave rows and columns of a block tile
+constexpr unsigned kOut = 0x80000000u, kRange = 0x7fffffffu;  // an offset outside the loads' range reads zero
+
+template <typename T> struct Elem {
+  static constexpr int E = sizeof(T);
+  static constexpr int V = 16 / E;    // elements per 16 bytes
+  static constexpr int BK = 128 / E;  // K per tile
+};
+
+// Where 16-column block c of LDS row k starts in a K-strided tile, in blocks: k
+// enters through the bits that differ between the rows of one fragment read
+template <typename T, int R> __device__ __forceinline__ int mix(int k) {
+  constexpr int mask = R / 16 - 1;
+  if (sizeof(T) == 2) return ((k & 3) | (((k >> 3) & 3) << 2)) & mask;
+  return ((k >> 2) & 3) & mask;
+}
+
+// Loads of one operand tile: R rows of K-contiguous data, or R columns of
+// K-strided data (PAIR: the second half of the columns lies `second` elements on).
+template <typename T, bool KS, int R, bool PAIR = false> struct Loader {
+  static constexpr int E = Elem<T>::E, V = Elem<T>::V, BK = Elem<T>::BK;
+  static constexpr int NL = R * 128 / (kThreads * 16);
+  const char* base;   // first element of the current K tile
+  size_t step;        // bytes between K tiles
+  unsigned off[NL];
+  int kk[NL];         // K of the load within its tile
+  // origin: element (row or column r0, k0) of the operand; n: valid rows or columns from r0 on
+  __device__ __forceinline__ void init(const T* origin, long long ld, int n, long long second = 0) {
+    base = reinterpret_cast<const char*>(origin);
+    step = KS ? (size_t)BK * ld * E : (size_t)128;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      if (!KS) {
+        const int r = i * (kThreads / 8) + wave * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+        // rows behind the last one repeat the first: they only feed rows of C that are not stored
+        off[i] = (unsigned)((r < n ? (long long)r * ld * E : 0) + c * 16);
+        kk[i] = c * V;
+      } else {
+        constexpr int RB = R * E;
+        const int flat = (i * (kThreads / 64) + wave) * 1024 + lane * 16;
+        const int k = flat / RB, el = flat % RB / E;
+        int col = ((el >> 4) ^ mix<T, R>(k)) * 16 + (el & 15);
+        long long at;
+        if (PAIR) {
+          const int h = col >= R / 2;
+          if (h) col -= R / 2;
+          at = (col < n ? col : 0) + (h ? second : 0);
+        } else {
+          at = col < n ? col : 0;
+        }
+        off[i] = (unsigned)(((long long)k * ld + at) * E);
+        kk[i] = k;
+      }
+    }
+  }
+  // next K tile into LDS at `dst`; left: K elements from the tile's start on
+  __device__ __forceinline__ void issue(char* dst, int left) {
+    const brsrc rs = make_brsrc(base, kRange);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const unsigned o = left >= BK || kk[i] < left ? off[i] : kOut;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + (i * (kThreads / 64) + wave) * 1024),
+                                               16, (int)o, 0, 0, 0);
+    }
+    base += step;
+  }
+};
+
+// Fragments of a tile: 16 rows (columns) b by one K slice (32 bf16 or 16 fp32)
+template <typename T> struct Frag;
+template <> struct Frag<bf16> { bf16x8 v; };
+template <> struct Frag<float> { f32x4 v; };
+
+template <typename T, bool KS, int R> struct Reader {
+  int lane_off[2];  // K contiguous: slice 0 and 1; K strided: [0] only
+  __device__ __forceinline__ void init() {
+    const int l = threadIdx.x & 63;
+    if (!KS) {
+      lane_off[0] = (l & 15) * 128 + (((l >> 4) ^ (l & 7)) * 16);
+      lane_off[1] = (l & 15) * 128 + (((4 + (l >> 4)) ^ (l & 7)) * 16);
+    } else if (sizeof(T) == 2) {
+      lane_off[0] = ((l >> 4) * 8 + ((l & 15) >> 2)) * (R * 2) + (l & 3) * 8;
+    } else {
+      lane_off[0] = (l >> 4) * 4 * (R * 4) + (l & 15) * 4;
+    }
+  }
+  __device__ __forceinline__ Frag<T> read(const char* tile, int block, int slice) const {
+    Frag<T> f;
+    if constexpr (!KS) {
+      const char* p = tile + block * 2048 + lane_off[slice];
+      f.v = *reinterpret_cast<const decltype(f.v)*>(p);
+    } else if constexpr (sizeof(T) == 2) {
+      const int l = threadIdx.x & 63;
+      const int c = block ^ mix<T, R>((l >> 4) * 8 + ((l & 15) >> 2));
+      const char* p = tile + lane_off[0] + c * 32 + slice * (32 * R * 2);
+      typedef __attribute__((address_space(3))) s16x4* tp;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(p));
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(p + 4 * R * 2));
+      f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int l = threadIdx.x & 63;
+      const int c = block ^ mix<T, R>((l >> 4) * 4);
+      const char* p = tile + lane_off[0] + c * 64 + slice * (16 * R * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f.v[j] = *reinterpret_cast<const float*>(p + j * (R * 4));
+    }
+    return f;
+  }
+};
+
+// acc (16 columns n by 16 rows m) += B^T A^T over one K slice
+__device__ __forceinline__ f32x4 mma(const Frag<bf16>& n, const Frag<bf16>& m, f32x4 acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(n.v, m.v, acc, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(const Frag<float>& n, const Frag<float>& m, f32x4 acc) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(n.v[j], m.v[j], acc, 0, 0, 0);
+  return acc;
+}
+
+// All of this wave's loads are in LDS, its LDS reads done; then the workgroup meets
+__device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// One product into acc[MI][NJ]: blocks of 16 rows from block row `ma`, column blocks nb[j]
+template <typename T, bool AKS, bool BKS, int RA, int RB, bool PAIR, int MI, int NJ>
+__device__ __forceinline__ void product(Loader<T, AKS, RA>& la, Loader<T, BKS, RB, PAIR>& lb, int K, char* smem, int ma,
+                                        const int (&nb)[NJ], f32x4 (&acc)[MI][NJ]) {
+  constexpr int BK = Elem<T>::BK, ABYTES = RA * 128, STAGE = (RA + RB) * 128;
+  Reader<T, AKS, RA> ra;
+  Reader<T, BKS, RB> rb;
+  ra.init();
+  rb.init();
+  const int tiles = (K + BK - 1) / BK;
+  la.issue(smem, K);
+  lb.issue(smem + ABYTES, K);
+  for (int t = 0; t < tiles; ++t) {
+    tile_barrier();
+    const char* cur = smem + (t & 1) * STAGE;
+    if (t + 1 < tiles) {
+      char* nxt = smem + ((t + 1) & 1) * STAGE;
+      la.issue(nxt, K - (t + 1) * BK);
+      lb.issue(nxt + ABYTES, K - (t + 1) * BK);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      Frag<T> b[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) b[j] = rb.read(cur + ABYTES, nb[j], s);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const Frag<T> a = ra.read(cur, ma + i, s);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = mma(b[j], a, acc[i][j]);
+      }
+    }
+  }
+  tile_barrier();  // the tiles may be written again
+}
+
+template <int MI, int NJ> __device__ __forceinline__ void zero(f32x4 (&acc)[MI][NJ]) {
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+__device__ __forceinline__ void store(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void store(bf16* p, f32x4 v) {
+  bf16x4 r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r[k] = (bf16)v[k];
+  *reinterpret_cast<bf16x4*>(p) = r;
+}
+
+constexpr int kXcds = 8;
+// Tile of workgroup `bid` when consecutive workgroups go round robin to the XCDs:
+// each XCD gets a contiguous range of tiles, whose operands meet in its L2
+__device__ __forceinline__ int xcd_tile(int bid, int total) {
+  const int q = total / kXcds, r = total % kXcds, x = bid % kXcds, k = bid / kXcds;
+  return x < r ? x * (q + 1) + k : r * (q + 1) + (x - r) * q + k;
+}
+
+extern __shared__ char ffn_smem[];
+
+// ------------------------------------------------------------ plain product
+// C [M][N] = A B; with splits > 1 (grid.y), split s sums K tiles [s per, (s + 1) per)
+// into out + s M N in fp32
+template <typename T, typename O, bool AKS, bool BKS, int TM, int TN>
+__global__ __launch_bounds__(kThreads) void ffn_gemm_kernel(const T* A, const T* B, O* C, int M, int N, int K,
+                                                            long long lda, long long ldb, int ntn, int per) {
+  constexpr int MI = TM / kWm / 16, NJ = TN / kWn / 16, BK = Elem<T>::BK;
+  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int m0 = tile / ntn * TM, n0 = tile % ntn * TN;
+  const long long k0 = (long long)blockIdx.y * per * BK;
+  const int kn = K - k0 < (long long)per * BK ? (int)(K - k0) : per * BK;
+  C += (size_t)blockIdx.y * M * N;
+  Loader<T, AKS, TM> la;
+  Loader<T, BKS, TN> lb;
+  la.init(AKS ? A + k0 * lda + m0 : A + (long long)m0 * lda + k0, lda, M - m0);
+  lb.init(BKS ? B + k0 * ldb + n0 : B + (long long)n0 * ldb + k0, ldb, N - n0);
+  const int wave = threadIdx.x >> 6, wm = wave % kWm, wn = wave / kWm, lane = threadIdx.x & 63;
+  int nb[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) nb[j] = wn * NJ + j;
+  f32x4 acc[MI][NJ];
+  zero(acc);
+  product<T, AKS, BKS, TM, TN, false, MI, NJ>(la, lb, kn, ffn_smem, wm * MI, nb, acc);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = m0 + (wm * MI + i) * 16 + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int n = n0 + nb[j] * 16 + (lane >> 4) * 4;
+      if (m < M && n < N) store(C + (size_t)m * N + n, acc[i][j]);
+    }
+  }
+}
+
+// ------------------------------------------------------------ gated product
+// z [M][F] = p act(q), (p, q) = x W_in. A block holds 128 columns of each.
+template <typename T, int ACT>
+__global__ __launch_bounds__(kThreads) void ffn_gate_kernel(const T* x, const T* w_in, T* z, int M, int D, int F,
+                                                            int ntn) {
+  constexpr int TM = 256, TF = 128, MI = TM / kWm / 16, NH = TF / kWn / 16, NJ = 2 * NH;
+  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int m0 = tile / ntn * TM, f0 = tile % ntn * TF;
+  Loader<T, false, TM> la;
+  Loader<T, true, 2 * TF, true> lb;
+  la.init(x + (long long)m0 * D, D, M - m0);
+  lb.init(w_in + f0, 2LL * F, F - f0, F);
+  const int wave = threadIdx.x >> 6, wm = wave % kWm, wn = wave / kWm, lane = threadIdx.x & 63;
+  int nb[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) nb[j] = (j < NH ? 0 : TF / 16) + wn * NH + j % NH;
+  f32x4 acc[MI][NJ];
+  zero(acc);
+  product<T, false, true, TM, 2 * TF, true, MI, NJ>(la, lb, D, ffn_smem, wm * MI, nb, acc);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = m0 + (wm * MI + i) * 16 + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < NH; ++j) {
+      const int f = f0 + nb[j] * 16 + (lane >> 4) * 4;
+      f32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = acc[i][j][k] * act_f<ACT>(acc[i][NH + j][k]);
+      if (m < M && f < F) store(z + (size_t)m * F + f, v);
+    }
+  }
+}
+
+// dz = dy W_out^T and p, q again; dp = dz act(q), dq = dz p act'(q) into dpq [M][2F], z [M][F]
+template <typename T, int ACT>
+__global__ __launch_bounds__(kThreads) void ffn_dgate_kernel(const T* x, const T* w_in, const T* dy, const T* w_out,
+                                                             T* dpq, T* z, int M, int D, int F, int ntn) {
+  constexpr int TM = 128, TF = 128, MI = TM / kWm / 16, NH = TF / kWn / 16, NJ = 2 * NH;
+  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+  const int m0 = tile / ntn * TM, f0 = tile % ntn * TF;
+  const int wave = threadIdx.x >> 6, wm = wave % kWm, wn = wave / kWm, lane = threadIdx.x & 63;
+  f32x4 dz[MI][NH], acc[MI][NJ];
+  int nb[NJ], nz[NH];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) nb[j] = (j < NH ? 0 : TF / 16) + wn * NH + j % NH;
+#pragma unroll
+  for (int j = 0; j < NH; ++j) nz[j] = wn * NH + j;
+  zero(dz);
+  zero(acc);
+  {
+    Loader<T, false, TM> la;
+    Loader<T, false, TF> lb;
+    la.init(dy + (long long)m0 * D, D, M - m0);
+    lb.init(w_out + (long long)f0 * D, D, F - f0);
+    product<T, false, false, TM, TF, false, MI, NH>(la, lb, D, ffn_smem, wm * MI, nz, dz);
+  }
+  {
+    Loader<T, false, TM> la;
+    Loader<T, true, 2 * TF, true> lb;
+    la.init(x + (long long)m0 * D, D, M - m0);
+    lb.init(w_in + f0, 2LL * F, F - f0, F);
+    product<T, false, true, TM, 2 * TF, true, MI, NJ>(la, lb, D, ffn_smem, wm * MI, nb, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = m0 + (wm * MI + i) * 16 + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < NH; ++j) {
+      const int f = f0 + nz[j] * 16 + (lane >> 4) * 4;
+      f32x4 vz, vp, vq;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float p = acc[i][j][k], g = dz[i][j][k];
+        float s, d;
+        act_d<ACT>(acc[i][NH + j][k], s, d);
+        vz[k] = p * s;
+        vp[k] = g * s;
+        vq[k] = g * p * d;
+      }
+      if (m < M && f < F) {
+        store(z + (size_t)m * F + f, vz);
+        store(dpq + (size_t)m * 2 * F + f, vp);
+        store(dpq + (size_t)m * 2 * F + F + f, vq);
+      }
+    }
+  }
+}
+
+// out = sum of the splits' partial results, in order
+template <typename T> __global__ __launch_bounds__(256) void ffn_join_kernel(const float* part, T* out, long long n4, int splits) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const f32x4* p = reinterpret_cast<const f32x4*>(part) + i;
+  f32x4 t = p[0];
+  for (int s = 1; s < splits; ++s) t += p[s * n4];
+  store(out + i * 4, t);
+}
+
+template <typename F> hipError_t allow_lds(F kernel, size_t bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, bool AKS, bool BKS>
+hipError_t gemm_go(const T* A, const T* B, T* C, int M, int N, int K, long long lda, long long ldb, int splits,
+                   float* part, hipStream_t s) {
+  constexpr int TM = 256, TN = 256;
+  constexpr size_t lds = 2 * (TM + TN) * 128;
+  const int ntn = (N + TN - 1) / TN, ntm = (M + TM - 1) / TM, tiles = (K + Elem<T>::BK - 1) / Elem<T>::BK;
+  const int per = (tiles + splits - 1) / splits;
+  hipError_t e;
+  if (splits == 1) {
+    auto k = ffn_gemm_kernel<T, T, AKS, BKS, TM, TN>;
+    if ((e = allow_lds(k, lds)) != hipSuccess) return e;
+    k<<<dim3(ntm * ntn), kThreads, lds, s>>>(A, B, C, M, N, K, lda, ldb, ntn, per);
+    return hipGetLastError();
+  }
+  auto k = ffn_gemm_kernel<T, float, AKS, BKS, TM, TN>;
+  if ((e = allow_lds(k, lds)) != hipSuccess) return e;
+  const int used = (tiles + per - 1) / per;
+  k<<<dim3(ntm * ntn, used), kThreads, lds, s>>>(A, B, part, M, N, K, lda, ldb, ntn, per);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const long long n4 = (long long)M * N / 4;
+  ffn_join_kernel<T><<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(part, C, n4, used);
+  return hipGetLastError();
+}
+
+template <typename T, int ACT> hipError_t fwd_go(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
+  constexpr size_t lds = 2 * (256 + 256) * 128;
+  const T* x = static_cast<const T*>(a.x);
+  T* z = static_cast<T*>(a.z);
+  const int ntn = (a.F + 127) / 128, ntm = (a.M + 255) / 256;
+  auto k = ffn_gate_kernel<T, ACT>;
+  hipError_t e = allow_lds(k, lds);
+  if (e != hipSuccess) return e;
+  k<<<ntm * ntn, kThreads, lds, s>>>(x, static_cast<const T*>(a.w_in), z, a.M, a.D, a.F, ntn);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  return gemm_go<T, false, true>(z, static_cast<const T*>(a.w_out), static_cast<T*>(a.y), a.M, a.D, a.F, a.F, a.D,
+                                 p.split_y, a.part, s);
+}
+
+template <typename T, int ACT> hipError_t bwd_go(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
+  constexpr size_t lds = 2 * (128 + 256) * 128;
+  const T *x = static_cast<const T*>(a.x), *w_in = static_cast<const T*>(a.w_in),
+          *w_out = static_cast<const T*>(a.w_out), *dy = static_cast<const T*>(a.dy);
+  T *z = static_cast<T*>(a.z), *dpq = static_cast<T*>(a.dpq);
+  const int ntn = (a.F + 127) / 128, ntm = (a.M + 127) / 128;
+  auto k = ffn_dgate_kernel<T, ACT>;
+  hipError_t e = allow_lds(k, lds);
+  if (e != hipSuccess) return e;
+  k<<<ntm * ntn, kThreads, lds, s>>>(x, w_in, dy, w_out, dpq, z, a.M, a.D, a.F, ntn);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  // dx = dpq W_in^T: W_in as stored is K contiguous for it
+  e = gemm_go<T, false, false>(dpq, w_in, static_cast<T*>(a.dx), a.M, a.D, 2 * a.F, 2LL * a.F, 2LL * a.F, p.split_dx,
+                               a.part, s);
+  if (e != hipSuccess) return e;
+  e = gemm_go<T, true, true>(x, dpq, static_cast<T*>(a.dw_in), a.D, 2 * a.F, a.M, a.D, 2LL * a.F, p.split_in, a.part, s);
+  if (e != hipSuccess) return e;
+  return gemm_go<T, true, true>(z, dy, static_cast<T*>(a.dw_out), a.F, a.D, a.M, a.F, a.D, p.split_out, a.part, s);
+}
+
+// K splits of a product so that its tiles make about 256 workgroups, at least 8 K tiles each
+int splits_of(long long M, long long N, long long K, int bk) {
+  const long long tiles = ((M + 255) / 256) * ((N + 255) / 256), kt = (K + bk - 1) / bk;
+  long long s = 256 / tiles;
+  if (s > kt / 8) s = kt / 8;
+  return s < 1 ? 1 : (int)(s > 64 ? 64 : s);
+}
+
+}  // namespace
+
+FfnPlan ffn_plan(int M, int D, int F, bool bf, bool bwd) {
+  const int bk = bf ? 64 : 32;
+  FfnPlan p{};
+  p.split_y = splits_of(M, D, F, bk);
+  p.split_dx = splits_of(M, D, 2LL * F, bk);
+  p.split_in = splits_of(D, 2LL * F, M, bk);
+  p.split_out = splits_of(F, D, M, bk);
+  auto need = [](int s, long long m, long long n) { return s > 1 ? (size_t)s * m * n : (size_t)0; };
+  if (!bwd) {
+    p.part_floats = need(p.split_y, M, D);
+  } else {
+    const size_t a = need(p.split_dx, M, D), b = need(p.split_in, D, 2LL * F), c = need(p.split_out, F, D);
+    p.part_floats = a > b ? (a > c ? a : c) : (b > c ? b : c);
+  }
+  return p;
+}
+
+#define HY_FFN_DISPATCH(fn)                                                    \
+  switch ((bf ? 3 : 0) + a.act) {                                              \
+    case 0: return fn<float, HYENA_ACT_NONE>(a, p, s);                         \
+    case 1: return fn<float, HYENA_ACT_SILU>(a, p, s);                         \
+    case 2: return fn<float, HYENA_ACT_GELU>(a, p, s);                         \
+    case 3: return fn<bf16, HYENA_ACT_NONE>(a, p, s);                          \
+    case 4: return fn<bf16, HYENA_ACT_SILU>(a, p, s);                          \
+    default: return fn<bf16, HYENA_ACT_GELU>(a, p, s);                         \
+  }
+hipError_t ffn_fwd(const FfnArgs& a, const FfnPlan& p, bool bf, hipStream_t s) { HY_FFN_DISPATCH(fwd_go) }
+hipError_t ffn_bwd(const FfnArgs& a, const FfnPlan& p, bool bf, hipStream_t s) { HY_FFN_DISPATCH(bwd_go) }
+#undef HY_FFN_DISPATCH
+
+}  // namespace hy

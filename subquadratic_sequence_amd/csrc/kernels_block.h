@@ -92,4 +92,20 @@ hipError_t gn_bwd(const GnArgs& a, const GnPlan& p, bool bf16, hipStream_t s);
 // out[d] = sum over rows of part [rows][ld], columns [0, D), in a fixed order
 hipError_t colsum(const float* part, float* out, long long rows, int ld, int D, hipStream_t s);
 
+// ---------------------------------------------- gated feed-forward block
+struct FfnArgs {
+  int M, D, F, act;
+  const void *x, *w_in, *w_out, *dy;
+  void *y, *dx, *dw_in, *dw_out;
+  void *z, *dpq;  // workspace [M][F], [M][2F] (storage type)
+  float* part;    // partial sums of split products
+};
+struct FfnPlan {
+  int split_y, split_dx, split_in, split_out;  // K splits of the products
+  size_t part_floats;
+};
+FfnPlan ffn_plan(int M, int D, int F, bool bf16, bool bwd);
+hipError_t ffn_fwd(const FfnArgs& a, const FfnPlan& p, bool bf16, hipStream_t s);
+hipError_t ffn_bwd(const FfnArgs& a, const FfnPlan& p, bool bf16, hipStream_t s);
+
 }  // namespace hy

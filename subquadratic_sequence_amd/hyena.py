@@ -113,6 +113,10 @@ SIGNATURES = {
     "hyena_glr_fwd": (_i, [ctypes.POINTER(GlrInputs), _vp, _ll, _ll, _vp, _vp, _sz, _vp]),
     "hyena_glr_bwd": (_i, [ctypes.POINTER(GlrInputs), _vp, _ll, _ll, _vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _vp,
                            _sz, _vp]),
+    "hyena_ffn_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "hyena_ffn_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "hyena_ffn_fwd": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "hyena_ffn_bwd": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "hyena_group_norm_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "hyena_group_norm_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "hyena_group_norm_fwd": (_i, [_i, _i, _i, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,

@@ -53,3 +53,11 @@ def group_norm(x, G, gamma=None, beta=None, eps=1e-5, name="none", lens=None):
         means.append(mean)
         rstds.append(rstd)
     return torch.stack(ys), torch.stack(means), torch.stack(rstds)
+
+
+def ffn(x, w_in, w_out, name):
+    """(y, z) of rows x [M, D]."""
+    F = w_out.shape[0]
+    pq = x @ w_in
+    z = pq[:, :F] * act(pq[:, F:], name)
+    return z @ w_out, z
