@@ -376,7 +376,8 @@ int hyena_nd_film_fwd_profiled(int X, int Y, int Z, int C, int N, int boundary, 
  *    the positions before t reaches t, not even an infinity or NaN.
  *  - t >= lens[b] (clamped to [0, L]): padding. It is not part of the sequence:
  *    what v, f, g, dy and reset hold there is not used, the state stays that of
- *    position lens[b] - 1 (h0 if lens[b] = 0), and y is left as it was.
+ *    position lens[b] - 1 (h0 if lens[b] = 0), and y is left as it was there
+ *    (pad_zero = 0) or set to 0 (pad_zero = 1).
  * Element (b, t, d) of v lies at v + b v_batch + t v_row + d, and likewise for the
  * others, so v, f and g may be column blocks of one projection's output. Rows are
  * contiguous; every stride is a multiple of 8 (bf16) or 4 (fp32) elements and not
@@ -396,6 +397,7 @@ typedef struct {
   const float *h0;              /* [B][D], or NULL: 0 */
   const unsigned char *reset;   /* [B][L], or NULL (any address) */
   const int *lens;              /* [B], or NULL (4-byte aligned) */
+  int pad_zero;                 /* y at padding: 0 leaves it, 1 writes 0 (forward only) */
 } hyena_glr_inputs;
 
 /* Scratch of the forward and the backward pass; 0 for unsupported sizes. */
@@ -427,13 +429,14 @@ int hyena_glr_bwd(const hyena_glr_inputs *in, const void *dy, long long dy_batch
  *            not overlap otherwise
  *   slots    [B]: row r advances the state of slot slots[r] (4-byte aligned; NULL:
  *            slot r, S >= B). A row whose slot is outside [0, S) is skipped: its y is
- *            left as it was. Rows of one slot are consecutive positions of that
- *            sequence, in row order. Slots that no row names are not written.
+ *            left as it was (pad_zero = 0) or set to 0 (pad_zero = 1). Rows of one slot
+ *            are consecutive positions of that sequence, in row order. Slots that no row
+ *            names are not written.
  *   y        [B][D] at y_row
  * Supported: B in [1, 8192], S in [1, 2^24], D as above. */
 int hyena_glr_step(int B, int D, int S, int dtype, const void *v, long long v_row, const void *f, long long f_row,
                    const void *g, long long g_row, const float *bias, const int *slots, const float *state,
-                   float *state_out, void *y, long long y_row, hipStream_t stream);
+                   float *state_out, void *y, long long y_row, int pad_zero, hipStream_t stream);
 
 /* ------------------------------------------ gated feed-forward block ---- */
 /* Activations of the gated feed-forward block and of the group norm. */
@@ -472,8 +475,8 @@ int hyena_ffn_bwd(int M, int D, int F, int dtype, int act, const void *x, const 
  *   mean, var = E[(x - mean)^2],  rstd = 1 / sqrt(var + eps)
  *   n = gamma (x - mean) rstd + beta,  y = act(n)
  * Positions s >= lens[b] (clamped to [0, S]) are padding: they enter no statistic,
- * whatever they hold, y is left as it was there and dx is 0. A sample with lens[b] = 0
- * has mean 0 and rstd 1 / sqrt(eps).
+ * whatever they hold; y is left as it was there (pad_zero = 0) or set to 0 (pad_zero = 1),
+ * dx is 0. A sample with lens[b] = 0 has mean 0 and rstd 1 / sqrt(eps).
  * Statistics and sums are fp32 in a fixed order (bit-reproducible), the variance from
  * deviations, not from the difference of two large sums.
  * Supported: B in [1, 2^24], S in [1, 2^24], C a multiple of 8 in [8, 8192], G a
@@ -485,8 +488,8 @@ size_t hyena_group_norm_bwd_workspace_bytes(int B, int S, int C, int G, int dtyp
 /*   x, y [B][S][C] dtype (y may be x: in place); gamma, beta [C] fp32 or NULL (1, 0)
  *   lens [B] or NULL (4-byte aligned); mean, rstd [B][G] fp32 (outputs; both may be NULL) */
 int hyena_group_norm_fwd(int B, int S, int C, int G, int dtype, int act, float eps, const void *x,
-                         const float *gamma, const float *beta, const int *lens, void *y, float *mean,
-                         float *rstd, void *ws, size_t ws_bytes, hipStream_t stream);
+                         const float *gamma, const float *beta, const int *lens, int pad_zero, void *y,
+                         float *mean, float *rstd, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* With dn = dy act'(n) and xh = (x - mean) rstd, the sums over a sample's group
  * m1 = avg(gamma dn), m2 = avg(gamma dn xh):

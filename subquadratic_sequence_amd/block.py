@@ -7,51 +7,56 @@ GPU's current stream, where workspaces are allocated too.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 
 import torch
 
 from .hyena import ACT_NONE, ACT_SILU, GlrInputs, HyenaError, _check, _dtype_code, lib
 
-_vp = ctypes.c_void_p
+# A decoding step is a few microseconds of GPU time, so what a call costs on the
+# host counts: addresses are passed as plain integers, workspace sizes are
+# remembered, and the current GPU is only switched where it has to be.
+_NO_SWITCH = contextlib.nullcontext()
 
 
 def _p(t):
-    return None if t is None else _vp(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-class _On:
-    """The GPU that holds all the tensors, made current for the call; its stream."""
+def _on(first, *tensors):
+    """(a context that makes the tensors' GPU current, that GPU's current stream); all
+    tensors have to be on one GPU."""
+    dev = first.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not {dev}")
+    guard = _NO_SWITCH if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return guard, torch._C._cuda_getCurrentRawStream(dev.index)
 
-    def __init__(self, *tensors):
-        ts = [t for t in tensors if t is not None]
-        dev = ts[0].device
-        for t in ts:
-            if t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}")
-        if dev.type != "cuda":
-            raise ValueError(f"tensors must be on a GPU, not {dev}")
-        self.device = dev
-        self.guard = torch.cuda.device(dev)
 
-    def __enter__(self):
-        self.guard.__enter__()
-        self.stream = _vp(torch.cuda.current_stream(self.device).cuda_stream)
-        return self
+@functools.lru_cache(maxsize=1024)
+def _need(query, *sizes):
+    """Bytes of a workspace; sizes outside the supported range raise."""
+    n = getattr(lib(), query)(*sizes)
+    if n == 0:
+        raise HyenaError(2, query)
+    return n
 
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
 
-    def scratch(self, ws, need, where):
-        if need == 0:
-            raise HyenaError(2, where)
-        if ws is None:
-            return torch.empty(need, dtype=torch.uint8, device=self.device)
-        if ws.device != self.device:
-            raise ValueError(f"workspace on {ws.device}, tensors on {self.device}")
-        if not ws.is_contiguous():
-            raise ValueError("the workspace must be contiguous")
-        return ws
+def _scratch(ws, like, query, *sizes):
+    """The workspace of a call: the caller's, or a new one."""
+    need = _need(query, *sizes)
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if ws.device != like.device:
+        raise ValueError(f"workspace on {ws.device}, tensors on {like.device}")
+    if not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return ws
 
 
 def _nbytes(t):
@@ -64,7 +69,7 @@ def _tensor(t, name, shape, dtype):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -77,13 +82,16 @@ def _rows(t, name, shape, dtype):
     dimension (0 for dimensions of size 1)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.stride(-1) != 1:
+    strides = t.stride()
+    if strides[-1] != 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])]
+    if 1 in shape:
+        return [s if n > 1 else 0 for s, n in zip(strides[:-1], shape)]
+    return strides[:-1]
 
 
 # ------------------------------------------------- gated linear recurrence
@@ -97,20 +105,22 @@ def hyena_glr_bwd_workspace_bytes(B, L, D, dtype) -> int:
     return lib().hyena_glr_bwd_workspace_bytes(B, L, D, dtype)
 
 
-def _glr_inputs(v, f, g, bias, h0, reset, lens):
+def _glr_inputs(v, f, g, bias, h0, reset, lens, pad_zero):
     if not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError("v: expected a tensor [B, L, D]")
-    B, L, D = v.shape
+    shape, dtype = v.shape, v.dtype
+    B, L, D = shape
     dt = _dtype_code(v)
-    sv, sf = _rows(v, "v", v.shape, v.dtype), _rows(f, "f", v.shape, v.dtype)
-    sg = [0, 0] if g is None else _rows(g, "g", v.shape, v.dtype)
+    sv, sf = _rows(v, "v", shape, dtype), _rows(f, "f", shape, dtype)
+    sg = (0, 0) if g is None else _rows(g, "g", shape, dtype)
     _tensor(bias, "bias", (D,), torch.float32)
     _tensor(h0, "h0", (B, D), torch.float32)
     if reset is not None and reset.dtype == torch.bool:
         reset = reset.view(torch.uint8)
     _tensor(reset, "reset", (B, L), torch.uint8)
     _tensor(lens, "lens", (B,), torch.int32)
-    return GlrInputs(B, L, D, dt, _p(v), _p(f), _p(g), *sv, *sf, *sg, _p(bias), _p(h0), _p(reset), _p(lens))
+    return GlrInputs(B, L, D, dt, _p(v), _p(f), _p(g), *sv, *sf, *sg, _p(bias), _p(h0), _p(reset), _p(lens),
+                     pad_zero)
 
 
 def hyena_glr_fwd(v, f, g=None, bias=None, h0=None, reset=None, lens=None, y=None, h_last=None, ws=None):
@@ -120,16 +130,17 @@ def hyena_glr_fwd(v, f, g=None, bias=None, h0=None, reset=None, lens=None, y=Non
     tensor are fine); bias [D], h0 and h_last [B, D] float32; reset [B, L] uint8 or
     bool; lens [B] int32. The state after the last position goes to h_last, if
     given. Positions behind lens are left as they are in a given y, zero otherwise."""
-    c = _glr_inputs(v, f, g, bias, h0, reset, lens)
+    c = _glr_inputs(v, f, g, bias, h0, reset, lens, y is None)
     if y is not None:
         sy = _rows(y, "y", v.shape, v.dtype)
     _tensor(h_last, "h_last", (c.B, c.D), torch.float32)
-    with _On(v, f, g, bias, h0, reset, lens, y, h_last) as on:
+    guard, stream = _on(v, f, g, bias, h0, reset, lens, y, h_last)
+    with guard:
         if y is None:
-            y = (torch.empty if lens is None else torch.zeros)(v.shape, dtype=v.dtype, device=v.device)
-            sy = _rows(y, "y", v.shape, v.dtype)
-        ws = on.scratch(ws, hyena_glr_workspace_bytes(c.B, c.L, c.D, c.dtype), "hyena_glr_workspace_bytes")
-        _check(lib().hyena_glr_fwd(ctypes.byref(c), _p(y), *sy, _p(h_last), _p(ws), _nbytes(ws), on.stream),
+            y = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            sy = y.stride()[:-1]
+        ws = _scratch(ws, v, "hyena_glr_workspace_bytes", c.B, c.L, c.D, c.dtype)
+        _check(lib().hyena_glr_fwd(ctypes.byref(c), _p(y), *sy, _p(h_last), _p(ws), _nbytes(ws), stream),
                "hyena_glr_fwd")
     return y
 
@@ -139,23 +150,24 @@ def hyena_glr_bwd(v, f, dy, g=None, bias=None, h0=None, reset=None, lens=None, d
     dv, df (and dg, if g is given; dtype of v), dbias [D] and dh0 [B, D] (float32).
     dv, df, dg are the column blocks of one tensor dp [B, L, 3D] (2D without g), in
     the dict too: the gradient of the projection that v, f, g come from."""
-    c = _glr_inputs(v, f, g, bias, h0, reset, lens)
+    c = _glr_inputs(v, f, g, bias, h0, reset, lens, False)
     B, L, D = v.shape
     n = 2 if g is None else 3
     sdy = _rows(dy, "dy", v.shape, v.dtype)
     _tensor(dh_last, "dh_last", (B, D), torch.float32)
     _tensor(dp, "dp", (B, L, n * D), v.dtype)
-    with _On(v, f, g, bias, h0, reset, lens, dy, dh_last, dp) as on:
+    guard, stream = _on(v, f, g, bias, h0, reset, lens, dy, dh_last, dp)
+    with guard:
         if dp is None:
             dp = torch.empty(B, L, n * D, dtype=v.dtype, device=v.device)
         out = dict(dp=dp, dv=dp[..., :D], df=dp[..., D:2 * D], dbias=torch.empty(D, device=v.device),
                    dh0=torch.empty(B, D, device=v.device))
         if g is not None:
             out["dg"] = dp[..., 2 * D:]
-        ws = on.scratch(ws, hyena_glr_bwd_workspace_bytes(B, L, D, c.dtype), "hyena_glr_bwd_workspace_bytes")
+        ws = _scratch(ws, v, "hyena_glr_bwd_workspace_bytes", B, L, D, c.dtype)
         _check(lib().hyena_glr_bwd(ctypes.byref(c), _p(dy), *sdy, _p(dh_last), _p(out["dv"]), _p(out["df"]),
                                    _p(out.get("dg")), L * n * D, n * D, _p(out["dbias"]), _p(out["dh0"]), _p(ws),
-                                   _nbytes(ws), on.stream), "hyena_glr_bwd")
+                                   _nbytes(ws), stream), "hyena_glr_bwd")
     return out
 
 
@@ -168,25 +180,28 @@ def hyena_glr_step(state, v, f, g=None, bias=None, slots=None, state_out=None, y
         raise ValueError("v: expected a tensor [B, D]")
     if not isinstance(state, torch.Tensor) or state.dim() != 2:
         raise ValueError("state: expected a tensor [S, D]")
-    B, D = v.shape
+    shape, dtype = v.shape, v.dtype
+    B, D = shape
     S = state.shape[0]
     dt = _dtype_code(v)
     _tensor(state, "state", (S, D), torch.float32)
     _tensor(state_out, "state_out", (S, D), torch.float32)
     _tensor(bias, "bias", (D,), torch.float32)
     _tensor(slots, "slots", (B,), torch.int32)
-    sv, sf = _rows(v, "v", v.shape, v.dtype), _rows(f, "f", v.shape, v.dtype)
-    sg = [0] if g is None else _rows(g, "g", v.shape, v.dtype)
+    sv, sf = _rows(v, "v", shape, dtype), _rows(f, "f", shape, dtype)
+    sg = (0,) if g is None else _rows(g, "g", shape, dtype)
+    pad_zero = y is None
     if y is not None:
-        sy = _rows(y, "y", v.shape, v.dtype)
+        sy = _rows(y, "y", shape, dtype)
     if state_out is None:
         state_out = state
-    with _On(v, f, g, bias, slots, state, state_out, y) as on:
+    guard, stream = _on(v, f, g, bias, slots, state, state_out, y)
+    with guard:
         if y is None:
-            y = (torch.empty if slots is None else torch.zeros)(B, D, dtype=v.dtype, device=v.device)
-            sy = _rows(y, "y", v.shape, v.dtype)
+            y = torch.empty(B, D, dtype=dtype, device=v.device)
+            sy = (D,)
         _check(lib().hyena_glr_step(B, D, S, dt, _p(v), *sv, _p(f), *sf, _p(g), *sg, _p(bias), _p(slots), _p(state),
-                                    _p(state_out), _p(y), *sy, on.stream), "hyena_glr_step")
+                                    _p(state_out), _p(y), *sy, pad_zero, stream), "hyena_glr_step")
     return y
 
 
@@ -225,12 +240,13 @@ def hyena_ffn_fwd(x, w_in, w_out, act=ACT_SILU, y=None, ws=None):
     M, D, F = _ffn_shape(x, w_in, w_out)
     dt = _dtype_code(x)
     _tensor(y, "y", x.shape, x.dtype)
-    with _On(x, w_in, w_out, y) as on:
+    guard, stream = _on(x, w_in, w_out, y)
+    with guard:
         if y is None:
             y = torch.empty_like(x)
-        ws = on.scratch(ws, hyena_ffn_workspace_bytes(M, D, F, dt), "hyena_ffn_workspace_bytes")
+        ws = _scratch(ws, x, "hyena_ffn_workspace_bytes", M, D, F, dt)
         _check(lib().hyena_ffn_fwd(M, D, F, dt, act, _p(x), _p(w_in), _p(w_out), _p(y), _p(ws), _nbytes(ws),
-                                   on.stream), "hyena_ffn_fwd")
+                                   stream), "hyena_ffn_fwd")
     return y
 
 
@@ -242,11 +258,12 @@ def hyena_ffn_bwd(x, w_in, w_out, dy, act=ACT_SILU, ws=None):
     if dy is None:
         raise TypeError("dy: expected a torch tensor")
     _tensor(dy, "dy", x.shape, x.dtype)
-    with _On(x, w_in, w_out, dy) as on:
+    guard, stream = _on(x, w_in, w_out, dy)
+    with guard:
         g = dict(dx=torch.empty_like(x), dw_in=torch.empty_like(w_in), dw_out=torch.empty_like(w_out))
-        ws = on.scratch(ws, hyena_ffn_bwd_workspace_bytes(M, D, F, dt), "hyena_ffn_bwd_workspace_bytes")
+        ws = _scratch(ws, x, "hyena_ffn_bwd_workspace_bytes", M, D, F, dt)
         _check(lib().hyena_ffn_bwd(M, D, F, dt, act, _p(x), _p(w_in), _p(w_out), _p(dy), _p(g["dx"]), _p(g["dw_in"]),
-                                   _p(g["dw_out"]), _p(ws), _nbytes(ws), on.stream), "hyena_ffn_bwd")
+                                   _p(g["dw_out"]), _p(ws), _nbytes(ws), stream), "hyena_ffn_bwd")
     return g
 
 
@@ -287,12 +304,15 @@ def hyena_group_norm_fwd(x, groups, gamma=None, beta=None, eps=1e-5, act=ACT_NON
     _tensor(y, "y", x.shape, x.dtype)
     _tensor(mean, "mean", (B, groups), torch.float32)
     _tensor(rstd, "rstd", (B, groups), torch.float32)
-    with _On(x, gamma, beta, lens, y, mean, rstd) as on:
+    guard, stream = _on(x, gamma, beta, lens, y, mean, rstd)
+    pad_zero = False
+    with guard:
         if y is None:
-            y = (torch.empty_like if lens is None else torch.zeros_like)(x)
-        ws = on.scratch(ws, hyena_group_norm_workspace_bytes(B, S, C, groups, dt), "hyena_group_norm_workspace_bytes")
-        _check(lib().hyena_group_norm_fwd(B, S, C, groups, dt, act, eps, _p(x), _p(gamma), _p(beta), _p(lens), _p(y),
-                                          _p(mean), _p(rstd), _p(ws), _nbytes(ws), on.stream), "hyena_group_norm_fwd")
+            y, pad_zero = torch.empty_like(x), True
+        ws = _scratch(ws, x, "hyena_group_norm_workspace_bytes", B, S, C, groups, dt)
+        _check(lib().hyena_group_norm_fwd(B, S, C, groups, dt, act, eps, _p(x), _p(gamma), _p(beta), _p(lens), pad_zero,
+                                          _p(y), _p(mean), _p(rstd), _p(ws), _nbytes(ws), stream),
+               "hyena_group_norm_fwd")
     return y
 
 
@@ -312,12 +332,12 @@ def hyena_group_norm_bwd(x, dy, groups, mean, rstd, gamma=None, beta=None, act=A
         if t is None:
             raise ValueError(f"{name}: the forward's statistics are needed")
         _tensor(t, name, (B, groups), torch.float32)
-    with _On(x, dy, gamma, beta, lens, mean, rstd, dx) as on:
+    guard, stream = _on(x, dy, gamma, beta, lens, mean, rstd, dx)
+    with guard:
         out = dict(dx=torch.empty_like(x) if dx is None else dx, dgamma=torch.empty(C, device=x.device),
                    dbeta=torch.empty(C, device=x.device))
-        ws = on.scratch(ws, hyena_group_norm_bwd_workspace_bytes(B, S, C, groups, dt),
-                        "hyena_group_norm_bwd_workspace_bytes")
+        ws = _scratch(ws, x, "hyena_group_norm_bwd_workspace_bytes", B, S, C, groups, dt)
         _check(lib().hyena_group_norm_bwd(B, S, C, groups, dt, act, _p(x), _p(dy), _p(gamma), _p(beta), _p(lens),
                                           _p(mean), _p(rstd), _p(out["dx"]), _p(out["dgamma"]), _p(out["dbeta"]),
-                                          _p(ws), _nbytes(ws), on.stream), "hyena_group_norm_bwd")
+                                          _p(ws), _nbytes(ws), stream), "hyena_group_norm_bwd")
     return out

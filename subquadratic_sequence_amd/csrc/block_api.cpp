@@ -106,6 +106,7 @@ hy::GlrArgs glr_args(const hyena_glr_inputs* in) {
   a.h0 = in->h0;
   a.reset = in->reset;
   a.lens = in->lens;
+  a.pad_zero = in->pad_zero != 0;
   return a;
 }
 
@@ -227,7 +228,7 @@ int hyena_glr_bwd(const hyena_glr_inputs* in, const void* dy, long long dy_batch
 
 int hyena_glr_step(int B, int D, int S, int dtype, const void* v, long long v_row, const void* f, long long f_row,
                    const void* g, long long g_row, const float* bias, const int* slots, const float* state,
-                   float* state_out, void* y, long long y_row, hipStream_t stream) {
+                   float* state_out, void* y, long long y_row, int pad_zero, hipStream_t stream) {
   if (!dtype_ok(dtype) || B < 1 || S < 1) return HYENA_ERR_INVALID_ARG;
   if (!aligned16(v) || !aligned16(f) || !aligned16(state) || !aligned16(state_out) || !aligned16(y))
     return HYENA_ERR_INVALID_ARG;
@@ -238,7 +239,7 @@ int hyena_glr_step(int B, int D, int S, int dtype, const void* v, long long v_ro
     return HYENA_ERR_INVALID_ARG;
   if (!out_strides_ok(0, y_row, 1, B, D, dtype)) return HYENA_ERR_INVALID_ARG;
   if (device_ok() != HYENA_OK) return HYENA_ERR_HIP;
-  hy::GlrStepArgs a{B, D, S, v, f, g, v_row, f_row, g_row, bias, slots, state, state_out, y, y_row};
+  hy::GlrStepArgs a{B, D, S, v, f, g, v_row, f_row, g_row, bias, slots, state, state_out, y, y_row, pad_zero != 0};
   HY_CHECK_HIP(hy::glr_step(a, dtype == HYENA_BF16, stream));
   return HYENA_OK;
 }
@@ -254,8 +255,8 @@ size_t hyena_group_norm_bwd_workspace_bytes(int B, int S, int C, int G, int dtyp
 }
 
 int hyena_group_norm_fwd(int B, int S, int C, int G, int dtype, int act, float eps, const void* x, const float* gamma,
-                         const float* beta, const int* lens, void* y, float* mean, float* rstd, void* ws,
-                         size_t ws_bytes, hipStream_t stream) {
+                         const float* beta, const int* lens, int pad_zero, void* y, float* mean, float* rstd,
+                         void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!dtype_ok(dtype) || !act_ok(act) || B < 1) return HYENA_ERR_INVALID_ARG;
   if (!(eps > 0.f) || !isfinite(eps)) return HYENA_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(y) || !aligned16(ws)) return HYENA_ERR_INVALID_ARG;
@@ -277,6 +278,7 @@ int hyena_group_norm_fwd(int B, int S, int C, int G, int dtype, int act, float e
   a.gamma = gamma;
   a.beta = beta;
   a.lens = lens;
+  a.pad_zero = pad_zero != 0;
   a.y = y;
   a.mean = mean;
   a.rstd = rstd;

@@ -242,6 +242,7 @@ __global__ __launch_bounds__(256) void glr_fwd_kernel(GlrArgs a, GlrPlan p) {
   const int cch = (int)(blockIdx.x % p.ctiles) * kGlrTile + (threadIdx.x & 63);
   const bool con = cch < a.D;
   const bool carries = threadIdx.x < kGlrTile && con;
+  const int ylen = MASK && a.pad_zero ? a.L : w.len;  // rows of y to write
   float h = con && a.h0 ? a.h0[(size_t)w.b * a.D + cch] : 0.f;
   if (p.C > 1) h = chunk_carry(a.agg + (size_t)w.b * p.C * a.D, 0, w.chunk, a.D, cch, con, h, sC);
   for (int sb = sb0; sb < sb1; ++sb) {
@@ -290,7 +291,8 @@ __global__ __launch_bounds__(256) void glr_fwd_kernel(GlrArgs a, GlrPlan p) {
         hh[k] = step<MASK>(al[i][k], hh[k], x[i][k]);
         yy[k] = GATE ? hh[k] * silu_f(gg[k]) : hh[k];
       }
-      if (w.on && t < w.len) store4(y + (long long)t * a.yr, yy);
+      if (MASK && t >= w.len) yy[0] = yy[1] = yy[2] = yy[3] = 0.f;
+      if (w.on && t < ylen) store4(y + (long long)t * a.yr, yy);
     }
   }
   if (carries && a.h_last && w.chunk == p.C - 1) a.h_last[(size_t)w.b * a.D + cch] = h;
@@ -485,7 +487,11 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrStepArgs a) {
   bool later = false;  // a later row has the same slot
   if (a.slots) {
     slot = a.slots[r];
-    if (slot < 0 || slot >= a.S) return;
+    if (slot < 0 || slot >= a.S) {
+      const float none[4] = {0.f, 0.f, 0.f, 0.f};
+      if (a.pad_zero && ch < a.D) store4(static_cast<T*>(a.y) + r * a.yr + ch, none);
+      return;
+    }
     // the whole workgroup reads the slots, 256 at a time
     bool before = false;
     for (int i = threadIdx.x; i < a.B; i += 256) {

@@ -25,6 +25,7 @@ struct GlrArgs {
   const float *bias, *h0;
   const unsigned char* reset;
   const int* lens;
+  bool pad_zero;  // write 0 to y at padding
   // forward
   void* y;
   long long yb, yr;
@@ -56,6 +57,7 @@ struct GlrStepArgs {
   float* state_out;
   void* y;
   long long yr;
+  bool pad_zero;
 };
 hipError_t glr_step(const GlrStepArgs& a, bool bf16, hipStream_t s);
 
@@ -66,6 +68,7 @@ struct GnArgs {
   const void *x, *dy;
   const float *gamma, *beta;
   const int* lens;
+  bool pad_zero;  // write 0 to y at padding
   void *y, *dx;
   float *mean, *rstd;           // forward outputs (may be null)
   const float *mean_in, *rstd_in;  // backward inputs

@@ -183,19 +183,21 @@ __device__ __forceinline__ void chunk_apply(const GnArgs& a, const GnPlan& p, co
   const size_t at = ((size_t)w.b * a.S + w.r0) * a.C + w.c;
   const T* x = static_cast<const T*>(a.x) + at;
   T* y = static_cast<T*>(a.y) + at;
-  for (int r = w.slot; r < w.rows; r += kU * p.slots) {
+  const int left = a.S - w.r0, all = !a.pad_zero ? w.rows : (left < p.per ? left : p.per);  // rows of y to write
+  for (int r = w.slot; r < all; r += kU * p.slots) {
     float v[kU][8];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int ru = r + u * p.slots;
-      ld8(x + (size_t)(ru < w.rows ? ru : r) * a.C, v[u]);
+      ld8(x + (size_t)(ru < all ? ru : r) * a.C, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int ru = r + u * p.slots;
-      if (ru < w.rows) {
+      if (ru < all) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[u][k] = act_f<ACT>(fmaf(v[u][k] - mean[k], ga[k], be[k]));
+        for (int k = 0; k < 8; ++k)
+          v[u][k] = ru < w.rows ? act_f<ACT>(fmaf(v[u][k] - mean[k], ga[k], be[k])) : 0.f;
         st8(y + (size_t)ru * a.C, v[u]);
       }
     }
@@ -454,7 +456,7 @@ template <typename T, int ACT, int NV> __global__ __launch_bounds__(1024) void g
       if (a.mean) a.mean[b * a.G + w.g] = live ? mean : 0.f;
       if (a.rstd) a.rstd[b * a.G + w.g] = rstd;
     }
-    if (!live) continue;
+    if (!live && !a.pad_zero) continue;
     T* y = static_cast<T*>(a.y) + b * a.C + w.c0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -462,7 +464,7 @@ template <typename T, int ACT, int NV> __global__ __launch_bounds__(1024) void g
         float ga[8], be[8];
         affine(a.gamma, a.beta, w.c0 + i * w.step, ga, be);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = act_f<ACT>(fmaf(v[i][k] * rstd, ga[k], be[k]));
+        for (int k = 0; k < 8; ++k) v[i][k] = live ? act_f<ACT>(fmaf(v[i][k] * rstd, ga[k], be[k])) : 0.f;
         st8(y + i * w.step, v[i]);
       }
   }
@@ -567,7 +569,7 @@ __global__ __launch_bounds__(1024) void colsum_kernel(const float* __restrict__ 
 
 template <typename F> hipError_t launch(F kernel, unsigned grid, int threads, size_t smem, const GnArgs& a,
                                         const GnPlan& p, hipStream_t s) {
-  if (smem > (64u << 10)) {
+  if (smem > (64u << 10)) {  // rare: C or G in the thousands
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != hipSuccess) return e;

@@ -67,7 +67,7 @@ class NDFilmParams(ctypes.Structure):
 class GlrInputs(ctypes.Structure):
     _fields_ = [("B", _i), ("L", _i), ("D", _i), ("dtype", _i), ("v", _vp), ("f", _vp), ("g", _vp),
                 ("v_batch", _ll), ("v_row", _ll), ("f_batch", _ll), ("f_row", _ll), ("g_batch", _ll), ("g_row", _ll),
-                ("bias", _vp), ("h0", _vp), ("reset", _vp), ("lens", _vp)]
+                ("bias", _vp), ("h0", _vp), ("reset", _vp), ("lens", _vp), ("pad_zero", _i)]
 
 
 # name -> (restype, argtypes)
@@ -119,11 +119,12 @@ SIGNATURES = {
     "hyena_ffn_bwd": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "hyena_group_norm_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "hyena_group_norm_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
-    "hyena_group_norm_fwd": (_i, [_i, _i, _i, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
-                                  _sz, _vp]),
+    "hyena_group_norm_fwd": (_i, [_i, _i, _i, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp,
+                                  _vp, _sz, _vp]),
     "hyena_group_norm_bwd": (_i, [_i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                   _sz, _vp]),
-    "hyena_glr_step": (_i, [_i, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _vp, _ll, _vp]),
+    "hyena_glr_step": (_i, [_i, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _vp, _ll, _i,
+                            _vp]),
 }
 
 _lib = None

@@ -324,3 +324,5 @@ def test_step_shared_and_missing_slots():
     check("state", state, want, torch.float32, 8, 4)
     check("y", y, wy, torch.float32, 8, 4)
     assert torch.equal(state[[1, 3]], a["state"][[1, 3]])
+    fresh = hs.hyena_glr_step(**{**a, "state": a["state"].clone()}, slots=slots.cuda())
+    assert torch.equal(fresh, torch.where(y == 5, torch.zeros_like(y), y))
