@@ -5,14 +5,18 @@
 // operands read as they are stored: K contiguous (rows of x, dy, z; W_in and
 // W_out where their transposes are needed) or K strided (W_in and W_out as they
 // are; both operands of the weight gradients, whose K runs over the rows of x).
-//  * Global to LDS: 16-byte loads that write LDS directly, two tiles in turn, one
-//    barrier per tile: tile t + 1 is on its way while tile t is multiplied.
+//  * Global to LDS: 16-byte loads that write LDS directly, tiles of 128 bytes of K (two
+//    MFMA slices in bf16) in two stages. The one barrier per tile stands between its
+//    two slices: the fragments of the second are in registers by then, so the
+//    tile's stage can be written again and the next tile's first fragments are read
+//    under the second slice's products. A tile is on its way for a whole tile's time.
+//    Reads and loads are spread between the MFMA instructions.
 //  * LDS: a tile is R rows (or columns) by 128 bytes of K. K contiguous: rows of
 //    128 bytes, 16-byte chunk c of row r at slot c ^ (r & 7), so that the 16 rows
 //    of a fragment read spread over the banks. K strided: rows of k, R elements
 //    each; blocks of 16 columns are exchanged by a function of k so that the rows
 //    of one transposing read (ds_read_b64_tr_b16; for fp32 four 4-byte reads) lie
-//    in different banks.
+//    in different banks. (No bank conflicts by the counters.)
 //  * MFMA: 16x16x32 bf16 or 4 x 16x16x4 fp32 per fragment pair. The operands go in
 //    swapped, so that a lane ends with four neighbouring columns of one row of C.
 //  * The gated product reads the p and the q columns of W_in as one tile and
@@ -45,18 +49,32 @@ template <typename T> struct Elem {
 // Where 16-column block c of LDS row k starts in a K-strided tile, in blocks: k
 // enters through the bits that differ between the rows of one fragment read
 template <typename T, int R> __device__ __forceinline__ int mix(int k) {
-  constexpr int mask = R / 16 - 1;
+  constexpr int mask = (R & (R - 1)) == 0 ? R / 16 - 1 : 3;  // R = 192: within groups of four blocks
   if (sizeof(T) == 2) return ((k & 3) | (((k >> 3) & 3) << 2)) & mask;
   return ((k >> 2) & 3) & mask;
 }
 
-// Loads of one operand tile: R rows of K-contiguous data, or R columns of
+// 16 bytes a lane from base + off (zeros where off is out of range) to the wave's 1 KB
+// of LDS at `dst`. Written out because the compiler, which cannot tell the stages
+// apart, waits for every such load it knows of before each transposing LDS read;
+// the waits that are needed stand in tile_barrier. The instruction has no
+// destination register, its operands are read when it issues.
+__device__ __forceinline__ void load_lds(const char* base, unsigned off, char* dst) {
+  typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+  const unsigned long long b = reinterpret_cast<unsigned long long>(base);
+  const u32x4 rs = {(unsigned)b, (unsigned)(b >> 32) & 0xffffu, kRange, 0x00020000u};
+  const unsigned at = (unsigned)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)dst);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rs)
+               : "memory", "m0");
+}
+
+// Loads of one operand's tiles: R rows of K-contiguous data, or R columns of
 // K-strided data (PAIR: the second half of the columns lies `second` elements on).
 template <typename T, bool KS, int R, bool PAIR = false> struct Loader {
   static constexpr int E = Elem<T>::E, V = Elem<T>::V, BK = Elem<T>::BK;
   static constexpr int NL = R * 128 / (kThreads * 16);
-  const char* base;   // first element of the current K tile
-  size_t step;        // bytes between K tiles
+  const char* base;   // first element of the next tile
+  size_t step;        // bytes between tiles
   unsigned off[NL];
   int kk[NL];         // K of the load within its tile
   // origin: element (row or column r0, k0) of the operand; n: valid rows or columns from r0 on
@@ -67,7 +85,7 @@ template <typename T, bool KS, int R, bool PAIR = false> struct Loader {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       if (!KS) {
-        const int r = i * (kThreads / 8) + wave * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+        const int r = (i * (kThreads / 64) + wave) * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
         // rows behind the last one repeat the first: they only feed rows of C that are not stored
         off[i] = (unsigned)((r < n ? (long long)r * ld * E : 0) + c * 16);
         kk[i] = c * V;
@@ -89,55 +107,52 @@ template <typename T, bool KS, int R, bool PAIR = false> struct Loader {
       }
     }
   }
-  // next K tile into LDS at `dst`; left: K elements from the tile's start on
+  // load i of the next tile into LDS at `dst`; left: K elements from the tile's start on
+  __device__ __forceinline__ void issue(int i, char* dst, int left) const {
+    const unsigned o = left >= BK || kk[i] < left ? off[i] : kOut;
+    load_lds(base, o, dst + (i * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 1024);
+  }
   __device__ __forceinline__ void issue(char* dst, int left) {
-    const brsrc rs = make_brsrc(base, kRange);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const unsigned o = left >= BK || kk[i] < left ? off[i] : kOut;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + (i * (kThreads / 64) + wave) * 1024),
-                                               16, (int)o, 0, 0, 0);
-    }
+    for (int i = 0; i < NL; ++i) issue(i, dst, left);
     base += step;
   }
 };
 
-// Fragments of a tile: 16 rows (columns) b by one K slice (32 bf16 or 16 fp32)
+// Fragments of a tile: 16 rows (columns) by one K slice (32 bf16 or 16 fp32)
 template <typename T> struct Frag;
 template <> struct Frag<bf16> { bf16x8 v; };
 template <> struct Frag<float> { f32x4 v; };
 
 template <typename T, bool KS, int R> struct Reader {
-  int lane_off[2];  // K contiguous: slice 0 and 1; K strided: [0] only
+  int lane_off, flip;
   __device__ __forceinline__ void init() {
     const int l = threadIdx.x & 63;
+    flip = 0;
     if (!KS) {
-      lane_off[0] = (l & 15) * 128 + (((l >> 4) ^ (l & 7)) * 16);
-      lane_off[1] = (l & 15) * 128 + (((4 + (l >> 4)) ^ (l & 7)) * 16);
+      lane_off = (l & 15) * 128 + (((l >> 4) ^ (l & 7)) * 16);
     } else if (sizeof(T) == 2) {
-      lane_off[0] = ((l >> 4) * 8 + ((l & 15) >> 2)) * (R * 2) + (l & 3) * 8;
+      const int k = (l >> 4) * 8 + ((l & 15) >> 2);
+      lane_off = k * (R * 2) + (l & 3) * 8;
+      flip = mix<T, R>(k);
     } else {
-      lane_off[0] = (l >> 4) * 4 * (R * 4) + (l & 15) * 4;
+      lane_off = (l >> 4) * 4 * (R * 4) + (l & 15) * 4;
+      flip = mix<T, R>((l >> 4) * 4);
     }
   }
   __device__ __forceinline__ Frag<T> read(const char* tile, int block, int slice) const {
     Frag<T> f;
     if constexpr (!KS) {
-      const char* p = tile + block * 2048 + lane_off[slice];
-      f.v = *reinterpret_cast<const decltype(f.v)*>(p);
+      // the second slice's chunks are 4 to 7: bit 2 of the slot
+      f.v = *reinterpret_cast<const decltype(f.v)*>(tile + block * 2048 + (lane_off ^ (slice * 64)));
     } else if constexpr (sizeof(T) == 2) {
-      const int l = threadIdx.x & 63;
-      const int c = block ^ mix<T, R>((l >> 4) * 8 + ((l & 15) >> 2));
-      const char* p = tile + lane_off[0] + c * 32 + slice * (32 * R * 2);
+      const char* p = tile + lane_off + (block ^ flip) * 32 + slice * (32 * R * 2);
       typedef __attribute__((address_space(3))) s16x4* tp;
       const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(p));
       const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(p + 4 * R * 2));
       f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const int l = threadIdx.x & 63;
-      const int c = block ^ mix<T, R>((l >> 4) * 4);
-      const char* p = tile + lane_off[0] + c * 64 + slice * (16 * R * 4);
+      const char* p = tile + lane_off + (block ^ flip) * 64 + slice * (16 * R * 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f.v[j] = *reinterpret_cast<const float*>(p + j * (R * 4));
     }
@@ -155,43 +170,75 @@ __device__ __forceinline__ f32x4 mma(const Frag<float>& n, const Frag<float>& m,
   return acc;
 }
 
-// All of this wave's loads are in LDS, its LDS reads done; then the workgroup meets
-__device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// At most N of this wave's loads still on their way, its LDS reads done; then the workgroup meets
+template <int N> __device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
-// One product into acc[MI][NJ]: blocks of 16 rows from block row `ma`, column blocks nb[j]
+constexpr size_t lds_bytes(int ra, int rb) { return (size_t)2 * (ra + rb) * 128; }
+
+// One product into acc[MI][NJ]: blocks of 16 rows from block row `ma`, column blocks nb[j].
 template <typename T, bool AKS, bool BKS, int RA, int RB, bool PAIR, int MI, int NJ>
 __device__ __forceinline__ void product(Loader<T, AKS, RA>& la, Loader<T, BKS, RB, PAIR>& lb, int K, char* smem, int ma,
                                         const int (&nb)[NJ], f32x4 (&acc)[MI][NJ]) {
   constexpr int BK = Elem<T>::BK, ABYTES = RA * 128, STAGE = (RA + RB) * 128;
+  constexpr int NL = Loader<T, AKS, RA>::NL + Loader<T, BKS, RB, PAIR>::NL;  // loads of a thread per tile
+  struct Frags {
+    Frag<T> a[MI], b[NJ];
+  };
   Reader<T, AKS, RA> ra;
   Reader<T, BKS, RB> rb;
   ra.init();
   rb.init();
-  const int tiles = (K + BK - 1) / BK;
+  constexpr int NA = Loader<T, AKS, RA>::NL, NB = Loader<T, BKS, RB, PAIR>::NL;
+  // part i of MI: that part's fragment reads and loads, and one row of products
+  auto read_part = [&](Frags& f, const char* tile, int slice, int i) {
+    f.a[i] = ra.read(tile, ma + i, slice);
+#pragma unroll
+    for (int j = i * NJ / MI; j < (i + 1) * NJ / MI; ++j) f.b[j] = rb.read(tile + ABYTES, nb[j], slice);
+  };
+  auto load_part = [&](char* tile, int left, int i) {
+#pragma unroll
+    for (int l = i * NA / MI; l < (i + 1) * NA / MI; ++l) la.issue(l, tile, left);
+#pragma unroll
+    for (int l = i * NB / MI; l < (i + 1) * NB / MI; ++l) lb.issue(l, tile + ABYTES, left);
+  };
+  auto multiply_part = [&](const Frags& f, int i) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = mma(f.b[j], f.a[i], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Tiles behind the last are asked for like any other; their offsets lie outside
+  // the range, so they read nothing and the loop needs no branches.
   la.issue(smem, K);
   lb.issue(smem + ABYTES, K);
-  for (int t = 0; t < tiles; ++t) {
-    tile_barrier();
-    const char* cur = smem + (t & 1) * STAGE;
-    if (t + 1 < tiles) {
-      char* nxt = smem + ((t + 1) & 1) * STAGE;
-      la.issue(nxt, K - (t + 1) * BK);
-      lb.issue(nxt + ABYTES, K - (t + 1) * BK);
+  la.issue(smem + STAGE, K - BK);
+  lb.issue(smem + STAGE + ABYTES, K - BK);
+  tile_barrier<NL>();
+  Frags f0, f1;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) read_part(f0, smem, 0, i);
+  char *cur = smem, *nxt = smem + STAGE;
+  for (int left = K; left > 0; left -= BK) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      read_part(f1, cur, 1, i);
+      multiply_part(f0, i);
     }
+    tile_barrier<0>();  // the next tile is in LDS; every wave has read all of this one
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      Frag<T> b[NJ];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) b[j] = rb.read(cur + ABYTES, nb[j], s);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const Frag<T> a = ra.read(cur, ma + i, s);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = mma(b[j], a, acc[i][j]);
-      }
+    for (int i = 0; i < MI; ++i) {
+      read_part(f0, nxt, 0, i);
+      load_part(cur, left - 2 * BK, i);
+      multiply_part(f1, i);
     }
+    la.base += la.step;
+    lb.base += lb.step;
+    char* t = cur;
+    cur = nxt;
+    nxt = t;
   }
-  tile_barrier();  // the tiles may be written again
+  tile_barrier<0>();  // the stages may be written again
 }
 
 template <int MI, int NJ> __device__ __forceinline__ void zero(f32x4 (&acc)[MI][NJ]) {
@@ -217,17 +264,29 @@ __device__ __forceinline__ int xcd_tile(int bid, int total) {
   return x < r ? x * (q + 1) + k : r * (q + 1) + (x - r) * q + k;
 }
 
+// Block row and column of a tile number: groups of 8 block rows, columns of a
+// group one after the other, so that the 32 tiles an XCD works on at a time span
+// about 8 x 4 blocks and share their operands in its L2
+__device__ __forceinline__ void tile_place(int tile, int ntm, int ntn, int& tm, int& tn) {
+  const int per = 8 * ntn, g = tile / per, r = tile - g * per;
+  const int rows = ntm - g * 8 < 8 ? ntm - g * 8 : 8;
+  tm = g * 8 + r % rows;
+  tn = r / rows;
+}
+
 extern __shared__ char ffn_smem[];
 
 // ------------------------------------------------------------ plain product
 // C [M][N] = A B; with splits > 1 (grid.y), split s sums K tiles [s per, (s + 1) per)
 // into out + s M N in fp32
 template <typename T, typename O, bool AKS, bool BKS, int TM, int TN>
-__global__ __launch_bounds__(kThreads) void ffn_gemm_kernel(const T* A, const T* B, O* C, int M, int N, int K,
+__global__ __launch_bounds__(kThreads, 1) void ffn_gemm_kernel(const T* A, const T* B, O* C, int M, int N, int K,
                                                             long long lda, long long ldb, int ntn, int per) {
   constexpr int MI = TM / kWm / 16, NJ = TN / kWn / 16, BK = Elem<T>::BK;
   const int tile = xcd_tile(blockIdx.x, gridDim.x);
-  const int m0 = tile / ntn * TM, n0 = tile % ntn * TN;
+  int tm, tn;
+  tile_place(tile, (M + TM - 1) / TM, ntn, tm, tn);
+  const int m0 = tm * TM, n0 = tn * TN;
   const long long k0 = (long long)blockIdx.y * per * BK;
   const int kn = K - k0 < (long long)per * BK ? (int)(K - k0) : per * BK;
   C += (size_t)blockIdx.y * M * N;
@@ -256,11 +315,13 @@ __global__ __launch_bounds__(kThreads) void ffn_gemm_kernel(const T* A, const T*
 // ------------------------------------------------------------ gated product
 // z [M][F] = p act(q), (p, q) = x W_in. A block holds 128 columns of each.
 template <typename T, int ACT>
-__global__ __launch_bounds__(kThreads) void ffn_gate_kernel(const T* x, const T* w_in, T* z, int M, int D, int F,
+__global__ __launch_bounds__(kThreads, 1) void ffn_gate_kernel(const T* x, const T* w_in, T* z, int M, int D, int F,
                                                             int ntn) {
   constexpr int TM = 256, TF = 128, MI = TM / kWm / 16, NH = TF / kWn / 16, NJ = 2 * NH;
   const int tile = xcd_tile(blockIdx.x, gridDim.x);
-  const int m0 = tile / ntn * TM, f0 = tile % ntn * TF;
+  int tm, tn;
+  tile_place(tile, (M + TM - 1) / TM, ntn, tm, tn);
+  const int m0 = tm * TM, f0 = tn * TF;
   Loader<T, false, TM> la;
   Loader<T, true, 2 * TF, true> lb;
   la.init(x + (long long)m0 * D, D, M - m0);
@@ -280,7 +341,7 @@ __global__ __launch_bounds__(kThreads) void ffn_gate_kernel(const T* x, const T*
       const int f = f0 + nb[j] * 16 + (lane >> 4) * 4;
       f32x4 v;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = acc[i][j][k] * act_f<ACT>(acc[i][NH + j][k]);
+      for (int k = 0; k < 4; ++k) v[k] = acc[i][j][k] * act_f<ACT, T>(acc[i][NH + j][k]);
       if (m < M && f < F) store(z + (size_t)m * F + f, v);
     }
   }
@@ -288,11 +349,13 @@ __global__ __launch_bounds__(kThreads) void ffn_gate_kernel(const T* x, const T*
 
 // dz = dy W_out^T and p, q again; dp = dz act(q), dq = dz p act'(q) into dpq [M][2F], z [M][F]
 template <typename T, int ACT>
-__global__ __launch_bounds__(kThreads) void ffn_dgate_kernel(const T* x, const T* w_in, const T* dy, const T* w_out,
+__global__ __launch_bounds__(kThreads, 1) void ffn_dgate_kernel(const T* x, const T* w_in, const T* dy, const T* w_out,
                                                              T* dpq, T* z, int M, int D, int F, int ntn) {
   constexpr int TM = 128, TF = 128, MI = TM / kWm / 16, NH = TF / kWn / 16, NJ = 2 * NH;
   const int tile = xcd_tile(blockIdx.x, gridDim.x);
-  const int m0 = tile / ntn * TM, f0 = tile % ntn * TF;
+  int tm, tn;
+  tile_place(tile, (M + TM - 1) / TM, ntn, tm, tn);
+  const int m0 = tm * TM, f0 = tn * TF;
   const int wave = threadIdx.x >> 6, wm = wave % kWm, wn = wave / kWm, lane = threadIdx.x & 63;
   f32x4 dz[MI][NH], acc[MI][NJ];
   int nb[NJ], nz[NH];
@@ -327,7 +390,7 @@ __global__ __launch_bounds__(kThreads) void ffn_dgate_kernel(const T* x, const T
       for (int k = 0; k < 4; ++k) {
         const float p = acc[i][j][k], g = dz[i][j][k];
         float s, d;
-        act_d<ACT>(acc[i][NH + j][k], s, d);
+        act_d<ACT, T>(acc[i][NH + j][k], s, d);
         vz[k] = p * s;
         vp[k] = g * s;
         vq[k] = g * p * d;
@@ -351,26 +414,33 @@ template <typename T> __global__ __launch_bounds__(256) void ffn_join_kernel(con
   store(out + i * 4, t);
 }
 
-template <typename F> hipError_t allow_lds(F kernel, size_t bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Lets a kernel take more than 64 KB of LDS, once per kernel (K) and device
+template <auto K> hipError_t allow_lds(size_t bytes) {
+  static DeviceCache done;
+  hipError_t e = hipSuccess;
+  done.get([&] {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(K), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return e == hipSuccess ? 1 : 0;
+  });
+  return e;
 }
 
 template <typename T, bool AKS, bool BKS>
 hipError_t gemm_go(const T* A, const T* B, T* C, int M, int N, int K, long long lda, long long ldb, int splits,
                    float* part, hipStream_t s) {
   constexpr int TM = 256, TN = 256;
-  constexpr size_t lds = 2 * (TM + TN) * 128;
+  constexpr size_t lds = lds_bytes(TM, TN);
   const int ntn = (N + TN - 1) / TN, ntm = (M + TM - 1) / TM, tiles = (K + Elem<T>::BK - 1) / Elem<T>::BK;
   const int per = (tiles + splits - 1) / splits;
   hipError_t e;
   if (splits == 1) {
-    auto k = ffn_gemm_kernel<T, T, AKS, BKS, TM, TN>;
-    if ((e = allow_lds(k, lds)) != hipSuccess) return e;
+    constexpr auto k = ffn_gemm_kernel<T, T, AKS, BKS, TM, TN>;
+    if ((e = allow_lds<k>(lds)) != hipSuccess) return e;
     k<<<dim3(ntm * ntn), kThreads, lds, s>>>(A, B, C, M, N, K, lda, ldb, ntn, per);
     return hipGetLastError();
   }
-  auto k = ffn_gemm_kernel<T, float, AKS, BKS, TM, TN>;
-  if ((e = allow_lds(k, lds)) != hipSuccess) return e;
+  constexpr auto k = ffn_gemm_kernel<T, float, AKS, BKS, TM, TN>;
+  if ((e = allow_lds<k>(lds)) != hipSuccess) return e;
   const int used = (tiles + per - 1) / per;
   k<<<dim3(ntm * ntn, used), kThreads, lds, s>>>(A, B, part, M, N, K, lda, ldb, ntn, per);
   if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -380,12 +450,12 @@ hipError_t gemm_go(const T* A, const T* B, T* C, int M, int N, int K, long long 
 }
 
 template <typename T, int ACT> hipError_t fwd_go(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
-  constexpr size_t lds = 2 * (256 + 256) * 128;
+  constexpr size_t lds = lds_bytes(256, 256);
   const T* x = static_cast<const T*>(a.x);
   T* z = static_cast<T*>(a.z);
   const int ntn = (a.F + 127) / 128, ntm = (a.M + 255) / 256;
-  auto k = ffn_gate_kernel<T, ACT>;
-  hipError_t e = allow_lds(k, lds);
+  constexpr auto k = ffn_gate_kernel<T, ACT>;
+  hipError_t e = allow_lds<k>(lds);
   if (e != hipSuccess) return e;
   k<<<ntm * ntn, kThreads, lds, s>>>(x, static_cast<const T*>(a.w_in), z, a.M, a.D, a.F, ntn);
   if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -394,13 +464,13 @@ template <typename T, int ACT> hipError_t fwd_go(const FfnArgs& a, const FfnPlan
 }
 
 template <typename T, int ACT> hipError_t bwd_go(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
-  constexpr size_t lds = 2 * (128 + 256) * 128;
+  constexpr size_t lds = lds_bytes(128, 256);
   const T *x = static_cast<const T*>(a.x), *w_in = static_cast<const T*>(a.w_in),
           *w_out = static_cast<const T*>(a.w_out), *dy = static_cast<const T*>(a.dy);
   T *z = static_cast<T*>(a.z), *dpq = static_cast<T*>(a.dpq);
   const int ntn = (a.F + 127) / 128, ntm = (a.M + 127) / 128;
-  auto k = ffn_dgate_kernel<T, ACT>;
-  hipError_t e = allow_lds(k, lds);
+  constexpr auto k = ffn_dgate_kernel<T, ACT>;
+  hipError_t e = allow_lds<k>(lds);
   if (e != hipSuccess) return e;
   k<<<ntm * ntn, kThreads, lds, s>>>(x, w_in, dy, w_out, dpq, z, a.M, a.D, a.F, ntn);
   if ((e = hipGetLastError()) != hipSuccess) return e;
