@@ -449,9 +449,9 @@ typedef enum { HYENA_ACT_NONE = 0, HYENA_ACT_SILU = 1, HYENA_ACT_GELU = 2 /* x P
  * Both projections of W_in, the activation and the product run in one kernel (p and
  * q stay in registers); z is kept in the storage type between the two products.
  * Backward, p and q recomputed from x:
- *   dz = dy W_out^T, dp = dz act(q), dq = dz p act'(q)      (one kernel)
+ *   dz = dy W_out^T, dp = dz act(q), dq = dz p act'(q)
  *   dx = [dp dq] W_in^T,  dw_in = x^T [dp dq],  dw_out = z^T dy
- * with z, dp and dq in the storage type, and every sum over K, rows included, in
+ * with z, dz, dp and dq in the storage type, and every sum over K, rows included, in
  * fp32. The gradients have the storage type of what they belong to.
  * Row-major and contiguous. Supported: M in [1, 2^24], D and F multiples of 8 in
  * [8, 2^16]. y (and the gradients) may not overlap the inputs.

@@ -20,8 +20,11 @@
 //  * MFMA: 16x16x32 bf16 or 4 x 16x16x4 fp32 per fragment pair. The operands go in
 //    swapped, so that a lane ends with four neighbouring columns of one row of C.
 //  * The gated product reads the p and the q columns of W_in as one tile and
-//    multiplies p by act(q) in registers. The backward's first kernel holds p, q
-//    and dz = dy W_out^T for the same rows and columns, so none of them is stored.
+//    multiplies p by act(q) in registers. The backward computes them again, reads
+//    dz = dy W_out^T where the epilogue needs it, and writes dp in its place: dz is
+//    rounded once to the storage type on the way. (Holding dz in a third
+//    accumulator instead left tiles of half the size: 268 us against 45 + 105 us at
+//    16384 x 768 x 2048.)
 #include <type_traits>
 
 #include "act.h"
@@ -256,6 +259,12 @@ __device__ __forceinline__ void store(bf16* p, f32x4 v) {
   *reinterpret_cast<bf16x4*>(p) = r;
 }
 
+__device__ __forceinline__ f32x4 load(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x4 load(const bf16* p) {
+  const bf16x4 r = *reinterpret_cast<const bf16x4*>(p);
+  return f32x4{(float)r[0], (float)r[1], (float)r[2], (float)r[3]};
+}
+
 constexpr int kXcds = 8;
 // Tile of workgroup `bid` when consecutive workgroups go round robin to the XCDs:
 // each XCD gets a contiguous range of tiles, whose operands meet in its L2
@@ -281,7 +290,8 @@ extern __shared__ char ffn_smem[];
 // into out + s M N in fp32
 template <typename T, typename O, bool AKS, bool BKS, int TM, int TN>
 __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_kernel(const T* A, const T* B, O* C, int M, int N, int K,
-                                                            long long lda, long long ldb, int ntn, int per) {
+                                                            long long lda, long long ldb, long long ldc, int ntn,
+                                                            int per) {
   constexpr int MI = TM / kWm / 16, NJ = TN / kWn / 16, BK = Elem<T>::BK;
   const int tile = xcd_tile(blockIdx.x, gridDim.x);
   int tm, tn;
@@ -307,38 +317,57 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_kernel(const T* A, const
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int n = n0 + nb[j] * 16 + (lane >> 4) * 4;
-      if (m < M && n < N) store(C + (size_t)m * N + n, acc[i][j]);
+      if (m < M && n < N) store(C + m * ldc + n, acc[i][j]);
     }
   }
 }
 
 // ------------------------------------------------------------ gated product
-// z [M][F] = p act(q), (p, q) = x W_in. A block holds 128 columns of each.
-template <typename T, int ACT>
-__global__ __launch_bounds__(kThreads, 1) void ffn_gate_kernel(const T* x, const T* w_in, T* z, int M, int D, int F,
-                                                            int ntn) {
-  constexpr int TM = 256, TF = 128, MI = TM / kWm / 16, NH = TF / kWn / 16, NJ = 2 * NH;
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
-  int tm, tn;
-  tile_place(tile, (M + TM - 1) / TM, ntn, tm, tn);
-  const int m0 = tm * TM, f0 = tn * TF;
-  Loader<T, false, TM> la;
-  Loader<T, true, 2 * TF, true> lb;
-  la.init(x + (long long)m0 * D, D, M - m0);
-  lb.init(w_in + f0, 2LL * F, F - f0, F);
-  const int wave = threadIdx.x >> 6, wm = wave % kWm, wn = wave / kWm, lane = threadIdx.x & 63;
-  int nb[NJ];
+// Block of the gated product: TM rows by TF columns of p and of q, in acc[.][j] and
+// acc[.][NH + j]
+template <int TM, int TF> struct GatePlace {
+  static constexpr int MI = TM / kWm / 16, NH = TF / kWn / 16, NJ = 2 * NH;
+  int m0, f0, wm, wn, lane;
+  __device__ __forceinline__ GatePlace(int M, int F, int ntn) {
+    int tm, tn;
+    tile_place(xcd_tile(blockIdx.x, gridDim.x), (M + TM - 1) / TM, ntn, tm, tn);
+    m0 = tm * TM;
+    f0 = tn * TF;
+    const int wave = threadIdx.x >> 6;
+    wm = wave % kWm;
+    wn = wave / kWm;
+    lane = threadIdx.x & 63;
+  }
+  __device__ __forceinline__ int row(int i) const { return m0 + (wm * MI + i) * 16 + (lane & 15); }
+  __device__ __forceinline__ int col(int j) const { return f0 + (wn * NH + j) * 16 + (lane >> 4) * 4; }
+  template <typename T>
+  __device__ __forceinline__ void run(const T* x, const T* w_in, int M, int D, int F, f32x4 (&acc)[MI][NJ]) const {
+    Loader<T, false, TM> la;
+    Loader<T, true, 2 * TF, true> lb;
+    la.init(x + (long long)m0 * D, D, M - m0);
+    lb.init(w_in + f0, 2LL * F, F - f0, F);
+    int nb[NJ];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) nb[j] = (j < NH ? 0 : TF / 16) + wn * NH + j % NH;
+    for (int j = 0; j < NJ; ++j) nb[j] = (j < NH ? 0 : TF / 16) + wn * NH + j % NH;
+    zero(acc);
+    product<T, false, true, TM, 2 * TF, true, MI, NJ>(la, lb, D, ffn_smem, wm * MI, nb, acc);
+  }
+};
+
+// z [M][F] = p act(q), (p, q) = x W_in
+template <typename T, int ACT, int TM, int TF>
+__global__ __launch_bounds__(kThreads, 1) void ffn_gate_kernel(const T* x, const T* w_in, T* z, int M, int D, int F,
+                                                               int ntn) {
+  constexpr int MI = TM / kWm / 16, NH = TF / kWn / 16, NJ = 2 * NH;
+  GatePlace<TM, TF> w(M, F, ntn);
   f32x4 acc[MI][NJ];
-  zero(acc);
-  product<T, false, true, TM, 2 * TF, true, MI, NJ>(la, lb, D, ffn_smem, wm * MI, nb, acc);
+  w.template run<T>(x, w_in, M, D, F, acc);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int m = m0 + (wm * MI + i) * 16 + (lane & 15);
+    const int m = w.row(i);
 #pragma unroll
     for (int j = 0; j < NH; ++j) {
-      const int f = f0 + nb[j] * 16 + (lane >> 4) * 4;
+      const int f = w.col(j);
       f32x4 v;
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = acc[i][j][k] * act_f<ACT, T>(acc[i][NH + j][k]);
@@ -347,59 +376,198 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_gate_kernel(const T* x, const
   }
 }
 
-// dz = dy W_out^T and p, q again; dp = dz act(q), dq = dz p act'(q) into dpq [M][2F], z [M][F]
-template <typename T, int ACT>
-__global__ __launch_bounds__(kThreads, 1) void ffn_dgate_kernel(const T* x, const T* w_in, const T* dy, const T* w_out,
-                                                             T* dpq, T* z, int M, int D, int F, int ntn) {
-  constexpr int TM = 128, TF = 128, MI = TM / kWm / 16, NH = TF / kWn / 16, NJ = 2 * NH;
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
-  int tm, tn;
-  tile_place(tile, (M + TM - 1) / TM, ntn, tm, tn);
-  const int m0 = tm * TM, f0 = tn * TF;
-  const int wave = threadIdx.x >> 6, wm = wave % kWm, wn = wave / kWm, lane = threadIdx.x & 63;
-  f32x4 dz[MI][NH], acc[MI][NJ];
-  int nb[NJ], nz[NH];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) nb[j] = (j < NH ? 0 : TF / 16) + wn * NH + j % NH;
-#pragma unroll
-  for (int j = 0; j < NH; ++j) nz[j] = wn * NH + j;
-  zero(dz);
-  zero(acc);
-  {
-    Loader<T, false, TM> la;
-    Loader<T, false, TF> lb;
-    la.init(dy + (long long)m0 * D, D, M - m0);
-    lb.init(w_out + (long long)f0 * D, D, F - f0);
-    product<T, false, false, TM, TF, false, MI, NH>(la, lb, D, ffn_smem, wm * MI, nz, dz);
-  }
-  {
-    Loader<T, false, TM> la;
-    Loader<T, true, 2 * TF, true> lb;
-    la.init(x + (long long)m0 * D, D, M - m0);
-    lb.init(w_in + f0, 2LL * F, F - f0, F);
-    product<T, false, true, TM, 2 * TF, true, MI, NJ>(la, lb, D, ffn_smem, wm * MI, nb, acc);
-  }
+// The backward's gates: p and q again, dz = dy W_out^T from the p half of dpq [M][2F];
+// dp = dz act(q) (in dz's place), dq = dz p act'(q), z = p act(q) to z [M][F]
+template <typename T, int ACT, int TM, int TF>
+__global__ __launch_bounds__(kThreads, 1) void ffn_dgate_kernel(const T* x, const T* w_in, T* dpq, T* z, int M, int D,
+                                                                int F, int ntn) {
+  constexpr int MI = TM / kWm / 16, NH = TF / kWn / 16, NJ = 2 * NH;
+  GatePlace<TM, TF> w(M, F, ntn);
+  f32x4 acc[MI][NJ];
+  w.template run<T>(x, w_in, M, D, F, acc);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int m = m0 + (wm * MI + i) * 16 + (lane & 15);
+    const int m = w.row(i);
 #pragma unroll
     for (int j = 0; j < NH; ++j) {
-      const int f = f0 + nz[j] * 16 + (lane >> 4) * 4;
+      const int f = w.col(j);
+      if (m >= M || f >= F) continue;
+      T* d = dpq + (size_t)m * 2 * F + f;
+      const f32x4 g = load(d);
       f32x4 vz, vp, vq;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float p = acc[i][j][k], g = dz[i][j][k];
-        float s, d;
-        act_d<ACT, T>(acc[i][NH + j][k], s, d);
+        const float p = acc[i][j][k];
+        float s, ds;
+        act_d<ACT, T>(acc[i][NH + j][k], s, ds);
         vz[k] = p * s;
-        vp[k] = g * s;
-        vq[k] = g * p * d;
+        vp[k] = g[k] * s;
+        vq[k] = g[k] * p * ds;
       }
-      if (m < M && f < F) {
-        store(z + (size_t)m * F + f, vz);
-        store(dpq + (size_t)m * 2 * F + f, vp);
-        store(dpq + (size_t)m * 2 * F + F + f, vq);
+      store(z + (size_t)m * F + f, vz);
+      store(d, vp);
+      store(d + F, vq);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+// Up to 64 rows (decoding): the products stream the weights once. A workgroup owns
+// NBT blocks of 16 columns (PAIR: NBT / 2 of p and of q), its eight waves a range of
+// K each, with LDS of their own: no barrier until their sums are joined, in wave
+// order. RING slices of x and W are on their way to LDS per wave.
+enum { kStore = 0, kGate = 1, kDgate = 2 };
+
+// Loads of one wave's slices of an operand: KC, NB blocks of 16 rows; KS, NB blocks of
+// 16 columns (PAIR: the second half `second` elements on); 1 KB a block
+template <typename T, bool KS, int NB, bool PAIR = false> struct WaveLoader {
+  static constexpr int E = Elem<T>::E, V = Elem<T>::V, BK = Elem<T>::BK / 2;
+  const char* base;
+  size_t step;
+  unsigned off[NB];
+  int kk[NB];
+  __device__ __forceinline__ void init(const T* origin, long long ld, int n, long long second = 0) {
+    base = reinterpret_cast<const char*>(origin);
+    step = KS ? (size_t)BK * ld * E : (size_t)64;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      if (!KS) {
+        const int r = i * 16 + (lane >> 2), c = (lane & 3) ^ ((lane >> 4) & 3);
+        off[i] = (unsigned)((r < n ? (long long)r * ld * E : 0) + c * 16);
+        kk[i] = c * V;
+      } else {
+        constexpr int R = NB * 16, RB = R * E;
+        const int flat = i * 1024 + lane * 16, k = flat / RB, el = flat % RB / E;
+        int col = ((el >> 4) ^ mix<T, R>(k)) * 16 + (el & 15);
+        long long at;
+        if (PAIR) {
+          const int h = col >= R / 2;
+          if (h) col -= R / 2;
+          at = (col < n ? col : 0) + (h ? second : 0);
+        } else {
+          at = col < n ? col : 0;
+        }
+        off[i] = (unsigned)(((long long)k * ld + at) * E);
+        kk[i] = k;
       }
+    }
+  }
+  __device__ __forceinline__ void issue(char* dst, int left) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) load_lds(base, left >= BK || kk[i] < left ? off[i] : kOut, dst + i * 1024);
+    base += step;
+  }
+};
+
+// fragment of block b of a KC slice (rows of 64 bytes, chunk c of row r at slot c ^ ((r >> 2) & 3))
+template <typename T> __device__ __forceinline__ Frag<T> wave_rows(const char* slice, int b) {
+  const int l = threadIdx.x & 63;
+  Frag<T> f;
+  f.v = *reinterpret_cast<const decltype(f.v)*>(slice + b * 1024 + (l & 15) * 64 + (((l >> 4) ^ ((l >> 2) & 3)) * 16));
+  return f;
+}
+
+constexpr int kFewWaves = 8;
+constexpr int few_ring(int mb, int nbt) { return 20 / (mb + nbt) < 8 ? 20 / (mb + nbt) : 8; }
+constexpr size_t few_lds(int mb, int nbt) {
+  const size_t ring = (size_t)kFewWaves * few_ring(mb, nbt) * (mb + nbt) * 1024, sums = (size_t)kFewWaves * mb * nbt * 1024;
+  return ring > sums ? ring : sums;
+}
+
+// B: W [K][ldb] (KS) or [N][ldb] (K contiguous). kStore: C [M][ldc]; kGate: z = C [M][N];
+// kDgate: C = z [M][N], dpq [M][2N]
+template <typename T, bool BKS, int MODE, int ACT, int MB, int NBT>
+__global__ __launch_bounds__(512, 1) void ffn_few_kernel(const T* A, const T* B, T* C, T* dpq, int M, int N, int K,
+                                                         long long lda, long long ldb, long long ldc) {
+  constexpr bool PAIR = MODE != kStore;
+  constexpr int BK = Elem<T>::BK / 2, RING = few_ring(MB, NBT), SLICE = (MB + NBT) * 1024;
+  constexpr int NO = PAIR ? NBT / 2 : NBT;  // column blocks of the output
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * NO * 16;
+  const int slices = (K + BK - 1) / BK, per = (slices + kFewWaves - 1) / kFewWaves;
+  const int s0 = wave * per < slices ? wave * per : slices, s1 = s0 + per < slices ? s0 + per : slices;
+  const long long k0 = (long long)s0 * BK;
+  WaveLoader<T, false, MB> la;
+  WaveLoader<T, BKS, NBT, PAIR && BKS> lb;
+  la.init(A + k0, lda, M);
+  lb.init(BKS ? B + k0 * ldb + n0 : B + (long long)n0 * ldb + k0, ldb, N - n0, N);
+  Reader<T, true, NBT * 16> rb;
+  rb.init();
+  char* ring = ffn_smem + wave * (RING * SLICE);
+  // K elements of this wave's range behind slice i (loads beyond it read nothing)
+  const int range = s1 < slices ? (s1 - s0) * BK : (int)(K - k0);
+  f32x4 acc[MB][NBT];
+  zero(acc);
+#pragma unroll
+  for (int i = 0; i < RING; ++i) {
+    la.issue(ring + i * SLICE, range - i * BK);
+    lb.issue(ring + i * SLICE + MB * 1024, range - i * BK);
+  }
+  char* cur = ring;
+  for (int i = 0; i < s1 - s0; ++i) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((RING - 1) * (MB + NBT)) : "memory");
+    Frag<T> a[MB], b[NBT];
+#pragma unroll
+    for (int x = 0; x < MB; ++x) a[x] = wave_rows<T>(cur, x);
+#pragma unroll
+    for (int x = 0; x < NBT; ++x) {
+      if constexpr (BKS) b[x] = rb.read(cur + MB * 1024, x, 0);
+      else b[x] = wave_rows<T>(cur + MB * 1024, x);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next loads write there
+    la.issue(cur, range - (i + RING) * BK);
+    lb.issue(cur + MB * 1024, range - (i + RING) * BK);
+#pragma unroll
+    for (int x = 0; x < MB; ++x)
+#pragma unroll
+      for (int y = 0; y < NBT; ++y) acc[x][y] = mma(b[y], a[x], acc[x][y]);
+    cur = cur + SLICE == ring + RING * SLICE ? ring : cur + SLICE;
+  }
+  tile_barrier<0>();
+  // [wave][row][column]
+  float* sums = reinterpret_cast<float*>(ffn_smem);
+#pragma unroll
+  for (int x = 0; x < MB; ++x)
+#pragma unroll
+    for (int y = 0; y < NBT; ++y)
+      store(sums + (((size_t)wave * MB + x) * 16 + (lane & 15)) * (NBT * 16) + y * 16 + (lane >> 4) * 4, acc[x][y]);
+  __syncthreads();
+  auto joined = [&](int m, int c) {
+    const float* p = sums + m * (NBT * 16) + c;
+    f32x4 t = load(p);
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) t += load(p + (size_t)w * (MB * 16 * NBT * 16));
+    return t;
+  };
+  for (int e = threadIdx.x; e < MB * 16 * NO * 4; e += 512) {
+    const int m = e / (NO * 4), c = e % (NO * 4) * 4, n = n0 + c;
+    if (m >= M || n >= N) continue;
+    const f32x4 p = joined(m, c);
+    if constexpr (MODE == kStore) {
+      store(C + m * ldc + n, p);
+    } else {
+      const f32x4 q = joined(m, NO * 16 + c);
+      f32x4 z;
+      if constexpr (MODE == kGate) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = p[k] * act_f<ACT, T>(q[k]);
+      } else {
+        T* d = dpq + (size_t)m * 2 * N + n;
+        const f32x4 g = load(d);
+        f32x4 vp, vq;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float v, dv;
+          act_d<ACT, T>(q[k], v, dv);
+          z[k] = p[k] * v;
+          vp[k] = g[k] * v;
+          vq[k] = g[k] * p[k] * dv;
+        }
+        store(d, vp);
+        store(d + N, vq);
+      }
+      store(C + (size_t)m * N + n, z);
     }
   }
 }
@@ -425,10 +593,12 @@ template <auto K> hipError_t allow_lds(size_t bytes) {
   return e;
 }
 
-template <typename T, bool AKS, bool BKS>
-hipError_t gemm_go(const T* A, const T* B, T* C, int M, int N, int K, long long lda, long long ldb, int splits,
-                   float* part, hipStream_t s) {
-  constexpr int TM = 256, TN = 256;
+constexpr int kFew = 4, kFewRows = 64;  // the tile index that stands for the few-rows kernel, its largest M
+constexpr int kTm[] = {256, 256, 128, 64}, kTn[] = {256, 192, 128, 128};  // block tiles of the plain product
+
+template <typename T, bool AKS, bool BKS, int TM, int TN>
+hipError_t gemm_tiles(const T* A, const T* B, T* C, int M, int N, int K, long long lda, long long ldb, long long ldc,
+                      int splits, float* part, hipStream_t s) {
   constexpr size_t lds = lds_bytes(TM, TN);
   const int ntn = (N + TN - 1) / TN, ntm = (M + TM - 1) / TM, tiles = (K + Elem<T>::BK - 1) / Elem<T>::BK;
   const int per = (tiles + splits - 1) / splits;
@@ -436,76 +606,166 @@ hipError_t gemm_go(const T* A, const T* B, T* C, int M, int N, int K, long long 
   if (splits == 1) {
     constexpr auto k = ffn_gemm_kernel<T, T, AKS, BKS, TM, TN>;
     if ((e = allow_lds<k>(lds)) != hipSuccess) return e;
-    k<<<dim3(ntm * ntn), kThreads, lds, s>>>(A, B, C, M, N, K, lda, ldb, ntn, per);
+    k<<<dim3(ntm * ntn), kThreads, lds, s>>>(A, B, C, M, N, K, lda, ldb, ldc, ntn, per);
     return hipGetLastError();
   }
   constexpr auto k = ffn_gemm_kernel<T, float, AKS, BKS, TM, TN>;
   if ((e = allow_lds<k>(lds)) != hipSuccess) return e;
   const int used = (tiles + per - 1) / per;
-  k<<<dim3(ntm * ntn, used), kThreads, lds, s>>>(A, B, part, M, N, K, lda, ldb, ntn, per);
+  k<<<dim3(ntm * ntn, used), kThreads, lds, s>>>(A, B, part, M, N, K, lda, ldb, N, ntn, per);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const long long n4 = (long long)M * N / 4;
   ffn_join_kernel<T><<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(part, C, n4, used);
   return hipGetLastError();
 }
 
-template <typename T, int ACT> hipError_t fwd_go(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
-  constexpr size_t lds = lds_bytes(256, 256);
-  const T* x = static_cast<const T*>(a.x);
-  T* z = static_cast<T*>(a.z);
-  const int ntn = (a.F + 127) / 128, ntm = (a.M + 255) / 256;
-  constexpr auto k = ffn_gate_kernel<T, ACT>;
-  hipError_t e = allow_lds<k>(lds);
+template <typename T, bool BKS, int MODE, int ACT, int MB, int NBT>
+hipError_t few_launch(const T* A, const T* B, T* C, T* dpq, int M, int N, int K, long long lda, long long ldb,
+                      long long ldc, hipStream_t s) {
+  constexpr size_t lds = few_lds(MB, NBT);
+  constexpr auto k = ffn_few_kernel<T, BKS, MODE, ACT, MB, NBT>;
+  const hipError_t e = allow_lds<k>(lds);
   if (e != hipSuccess) return e;
-  k<<<ntm * ntn, kThreads, lds, s>>>(x, static_cast<const T*>(a.w_in), z, a.M, a.D, a.F, ntn);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  return gemm_go<T, false, true>(z, static_cast<const T*>(a.w_out), static_cast<T*>(a.y), a.M, a.D, a.F, a.F, a.D,
-                                 p.split_y, a.part, s);
+  const int cols = (MODE == kStore ? NBT : NBT / 2) * 16;
+  k<<<(N + cols - 1) / cols, 512, lds, s>>>(A, B, C, dpq, M, N, K, lda, ldb, ldc);
+  return hipGetLastError();
+}
+// Narrow columns while they make at most one workgroup per CU, twice the width beyond
+template <typename T, bool BKS, int MODE, int ACT>
+hipError_t few_go(const T* A, const T* B, T* C, T* dpq, int M, int N, int K, long long lda, long long ldb,
+                  long long ldc, hipStream_t s) {
+  constexpr int W = MODE == kStore ? 1 : 2;
+  const bool wide = N > 256 * 16;
+#define HY_FFN_FEW(MB)                                                                                     \
+  return wide ? few_launch<T, BKS, MODE, ACT, MB, 2 * W>(A, B, C, dpq, M, N, K, lda, ldb, ldc, s)          \
+              : few_launch<T, BKS, MODE, ACT, MB, W>(A, B, C, dpq, M, N, K, lda, ldb, ldc, s);
+  if (M <= 16) HY_FFN_FEW(1)
+  if (M <= 32) HY_FFN_FEW(2)
+  HY_FFN_FEW(4)
+#undef HY_FFN_FEW
+}
+
+template <typename T, bool AKS, bool BKS>
+hipError_t gemm_go(const FfnProduct& p, const T* A, const T* B, T* C, int M, int N, int K, long long lda, long long ldb,
+                   long long ldc, float* part, hipStream_t s) {
+  if constexpr (!AKS)
+    if (p.tile == kFew) return few_go<T, BKS, kStore, HYENA_ACT_NONE>(A, B, C, nullptr, M, N, K, lda, ldb, ldc, s);
+  switch (p.tile) {
+    case 0: return gemm_tiles<T, AKS, BKS, 256, 256>(A, B, C, M, N, K, lda, ldb, ldc, p.splits, part, s);
+    case 1: return gemm_tiles<T, AKS, BKS, 256, 192>(A, B, C, M, N, K, lda, ldb, ldc, p.splits, part, s);
+    case 2: return gemm_tiles<T, AKS, BKS, 128, 128>(A, B, C, M, N, K, lda, ldb, ldc, p.splits, part, s);
+    default: return gemm_tiles<T, AKS, BKS, 64, 128>(A, B, C, M, N, K, lda, ldb, ldc, p.splits, part, s);
+  }
+}
+
+template <typename T, int ACT, int TM, int TF> hipError_t gate_tiles(const FfnArgs& a, bool bwd, hipStream_t s) {
+  constexpr size_t lds = lds_bytes(TM, 2 * TF);
+  const T *x = static_cast<const T*>(a.x), *w_in = static_cast<const T*>(a.w_in);
+  const int ntn = (a.F + TF - 1) / TF, grid = (a.M + TM - 1) / TM * ntn;
+  hipError_t e;
+  if (!bwd) {
+    constexpr auto k = ffn_gate_kernel<T, ACT, TM, TF>;
+    if ((e = allow_lds<k>(lds)) != hipSuccess) return e;
+    k<<<grid, kThreads, lds, s>>>(x, w_in, static_cast<T*>(a.z), a.M, a.D, a.F, ntn);
+  } else {
+    constexpr auto k = ffn_dgate_kernel<T, ACT, TM, TF>;
+    if ((e = allow_lds<k>(lds)) != hipSuccess) return e;
+    k<<<grid, kThreads, lds, s>>>(x, w_in, static_cast<T*>(a.dpq), static_cast<T*>(a.z), a.M, a.D, a.F, ntn);
+  }
+  return hipGetLastError();
+}
+
+template <typename T, int ACT> hipError_t gate_go(const FfnArgs& a, int tile, bool bwd, hipStream_t s) {
+  if (tile == kFew) {
+    const T *x = static_cast<const T*>(a.x), *w_in = static_cast<const T*>(a.w_in);
+    T *z = static_cast<T*>(a.z), *dpq = static_cast<T*>(a.dpq);
+    return bwd ? few_go<T, true, kDgate, ACT>(x, w_in, z, dpq, a.M, a.F, a.D, a.D, 2LL * a.F, 0, s)
+               : few_go<T, true, kGate, ACT>(x, w_in, z, dpq, a.M, a.F, a.D, a.D, 2LL * a.F, 0, s);
+  }
+  switch (tile) {
+    case 0: return gate_tiles<T, ACT, 256, 128>(a, bwd, s);
+    case 2: return gate_tiles<T, ACT, 128, 64>(a, bwd, s);
+    default: return gate_tiles<T, ACT, 64, 64>(a, bwd, s);
+  }
+}
+
+template <typename T, int ACT> hipError_t fwd_go(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
+  hipError_t e = gate_go<T, ACT>(a, p.gate.tile, false, s);
+  if (e != hipSuccess) return e;
+  return gemm_go<T, false, true>(p.y, static_cast<T*>(a.z), static_cast<const T*>(a.w_out), static_cast<T*>(a.y), a.M,
+                                 a.D, a.F, a.F, a.D, a.D, a.part, s);
 }
 
 template <typename T, int ACT> hipError_t bwd_go(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
-  constexpr size_t lds = lds_bytes(128, 256);
   const T *x = static_cast<const T*>(a.x), *w_in = static_cast<const T*>(a.w_in),
           *w_out = static_cast<const T*>(a.w_out), *dy = static_cast<const T*>(a.dy);
   T *z = static_cast<T*>(a.z), *dpq = static_cast<T*>(a.dpq);
-  const int ntn = (a.F + 127) / 128, ntm = (a.M + 127) / 128;
-  constexpr auto k = ffn_dgate_kernel<T, ACT>;
-  hipError_t e = allow_lds<k>(lds);
+  const long long F2 = 2LL * a.F;
+  // dz = dy W_out^T into the p half of dpq (W_out as stored is K contiguous for it)
+  hipError_t e = gemm_go<T, false, false>(p.dz, dy, w_out, dpq, a.M, a.F, a.D, a.D, a.D, F2, a.part, s);
   if (e != hipSuccess) return e;
-  k<<<ntm * ntn, kThreads, lds, s>>>(x, w_in, dy, w_out, dpq, z, a.M, a.D, a.F, ntn);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if ((e = gate_go<T, ACT>(a, p.gate.tile, true, s)) != hipSuccess) return e;
   // dx = dpq W_in^T: W_in as stored is K contiguous for it
-  e = gemm_go<T, false, false>(dpq, w_in, static_cast<T*>(a.dx), a.M, a.D, 2 * a.F, 2LL * a.F, 2LL * a.F, p.split_dx,
-                               a.part, s);
+  e = gemm_go<T, false, false>(p.dx, dpq, w_in, static_cast<T*>(a.dx), a.M, a.D, 2 * a.F, F2, F2, a.D, a.part, s);
   if (e != hipSuccess) return e;
-  e = gemm_go<T, true, true>(x, dpq, static_cast<T*>(a.dw_in), a.D, 2 * a.F, a.M, a.D, 2LL * a.F, p.split_in, a.part, s);
+  e = gemm_go<T, true, true>(p.dw_in, x, dpq, static_cast<T*>(a.dw_in), a.D, 2 * a.F, a.M, a.D, F2, F2, a.part, s);
   if (e != hipSuccess) return e;
-  return gemm_go<T, true, true>(z, dy, static_cast<T*>(a.dw_out), a.F, a.D, a.M, a.F, a.D, p.split_out, a.part, s);
+  return gemm_go<T, true, true>(p.dw_out, z, dy, static_cast<T*>(a.dw_out), a.F, a.D, a.M, a.F, a.D, a.D, a.part, s);
 }
 
-// K splits of a product so that its tiles make about 256 workgroups, at least 8 K tiles each
-int splits_of(long long M, long long N, long long K, int bk) {
-  const long long tiles = ((M + 255) / 256) * ((N + 255) / 256), kt = (K + bk - 1) / bk;
-  long long s = 256 / tiles;
-  if (s > kt / 8) s = kt / 8;
-  return s < 1 ? 1 : (int)(s > 64 ? 64 : s);
+// Tile and K splits of a product by an estimate of its time. A workgroup alone on a
+// CU takes `alone` us per K tile, several take `pace` us each (measured, bf16: a 256 x
+// 256 tile 1.35, 128 x 128 0.7 alone and 0.42 together; fp32 is bound by its MFMA rate,
+// in proportion to the area); launch, first loads and stores take `fixed`; splits
+// write and read their partial sums at about 4 TB/s and add a launch.
+FfnProduct choose(long long M, long long N, long long K, bool bf, bool may_split, bool gate) {
+  static const double pace_bf[] = {1.35, 1.08, 0.42, 0.26}, alone_bf[] = {1.35, 1.08, 0.70, 0.40};
+  static const double pace_f32[] = {4.0, 3.0, 1.05, 0.55}, alone_f32[] = {4.0, 3.0, 1.3, 0.8};
+  static const double fixed[] = {8, 7, 4.5, 3.5};
+  const long long kt = (K + (bf ? 63 : 31)) / (bf ? 64 : 32);
+  FfnProduct best{0, 1};
+  double best_us = 1e30;
+  for (int c = 0; c < 4; ++c) {
+    if (gate && c == 1) continue;
+    const double pace = bf ? pace_bf[c] : pace_f32[c], alone = bf ? alone_bf[c] : alone_f32[c];
+    const long long tiles = ((M + kTm[c] - 1) / kTm[c]) * ((N + kTn[c] - 1) / kTn[c]);
+    for (int s = 1; s <= 32; ++s) {
+      if (s > 1 && (!may_split || kt / s < 4 || tiles * s > 512)) break;
+      const long long rounds = (tiles * s + 255) / 256;
+      const double per = rounds * pace > alone ? rounds * pace : alone;
+      double us = (kt + s - 1) / s * per + fixed[c];
+      if (s > 1) us += 4 + (double)M * N * s * 8e-6 / 4;
+      if (us < best_us) {
+        best_us = us;
+        best = FfnProduct{c, s};
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 FfnPlan ffn_plan(int M, int D, int F, bool bf, bool bwd) {
-  const int bk = bf ? 64 : 32;
   FfnPlan p{};
-  p.split_y = splits_of(M, D, F, bk);
-  p.split_dx = splits_of(M, D, 2LL * F, bk);
-  p.split_in = splits_of(D, 2LL * F, M, bk);
-  p.split_out = splits_of(F, D, M, bk);
-  auto need = [](int s, long long m, long long n) { return s > 1 ? (size_t)s * m * n : (size_t)0; };
+  const FfnProduct few{kFew, 1};
+  const bool is_few = M <= kFewRows;
+  auto need = [&](const FfnProduct& q, long long m, long long n) {
+    const size_t f = q.splits > 1 ? (size_t)q.splits * m * n : 0;
+    if (f > p.part_floats) p.part_floats = f;
+  };
+  p.gate = is_few ? few : choose(M, 2LL * F, D, bf, false, true);
   if (!bwd) {
-    p.part_floats = need(p.split_y, M, D);
+    p.y = is_few ? few : choose(M, D, F, bf, true, false);
+    need(p.y, M, D);
   } else {
-    const size_t a = need(p.split_dx, M, D), b = need(p.split_in, D, 2LL * F), c = need(p.split_out, F, D);
-    p.part_floats = a > b ? (a > c ? a : c) : (b > c ? b : c);
+    p.dz = is_few ? few : choose(M, F, D, bf, false, false);  // written into a wider matrix: not split
+    p.dx = is_few ? few : choose(M, D, 2LL * F, bf, true, false);
+    p.dw_in = choose(D, 2LL * F, M, bf, true, false);
+    p.dw_out = choose(F, D, M, bf, true, false);
+    need(p.dx, M, D);
+    need(p.dw_in, D, 2LL * F);
+    need(p.dw_out, F, D);
   }
   return p;
 }

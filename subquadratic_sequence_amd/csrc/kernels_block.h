@@ -103,8 +103,11 @@ struct FfnArgs {
   void *z, *dpq;  // workspace [M][F], [M][2F] (storage type)
   float* part;    // partial sums of split products
 };
+struct FfnProduct {
+  int tile, splits;  // block tile (index), K splits
+};
 struct FfnPlan {
-  int split_y, split_dx, split_in, split_out;  // K splits of the products
+  FfnProduct gate, y, dz, dx, dw_in, dw_out;
   size_t part_floats;
 };
 FfnPlan ffn_plan(int M, int D, int F, bool bf16, bool bwd);

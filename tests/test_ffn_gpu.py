@@ -8,7 +8,8 @@ Real numbers (u = 2^-24 and, for bf16, h = 2^-8, else 0): p and q carry K u of t
 magnitudes P = |x| |w_in|; the activation's slope is at most 1.13 and its own error
 8 u of its size plus, for gelu, 4 u |q|; z = p act(q) is rounded once (h). With Z the
 bound of |z|'s error, y is off by Z |w_out|, F u of |z| |w_out|, and its rounding. The
-backward's dp, dq follow in the same way, through dz with D u of |dy| |w_out|^T; dx and
+backward's dp, dq follow in the same way, through dz with D u of |dy| |w_out|^T and
+dz's own rounding (h); dx and
 the weight gradients sum such terms over 2F or M, with as many u and one rounding.
 These are sums of worst cases, elementwise."""
 import pytest
@@ -100,7 +101,7 @@ def test_real_numbers(M, D, F, act, dtype):
     da = torch.autograd.grad(block_ref.act(qq, act).sum(), qq)[0]
     eda = 1.0 * eq + 8 * U * (1 + q.abs())  # |act''| <= 1
     dz = dd @ wo.t()
-    edz = (D + 4) * U * (dd.abs() @ wo.abs().t())
+    edz = (D + 4) * U * (dd.abs() @ wo.abs().t()) * (1 + h) + (h + U) * dz.abs()
     dp, dq = dz * a, dz * p * da
     edp = (edz * a.abs() + dz.abs() * ea) * (1 + h) + (h + 2 * U) * dp.abs()
     edq = (edz * (p * da).abs() + dz.abs() * (ep * da.abs() + p.abs() * eda)) * (1 + h) + (h + 4 * U) * dq.abs()
