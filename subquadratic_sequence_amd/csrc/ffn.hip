@@ -17,8 +17,14 @@
 //    each; blocks of 16 columns are exchanged by a function of k so that the rows
 //    of one transposing read (ds_read_b64_tr_b16; for fp32 four 4-byte reads) lie
 //    in different banks. (No bank conflicts by the counters.)
-//  * MFMA: 16x16x32 bf16 or 4 x 16x16x4 fp32 per fragment pair. The operands go in
-//    swapped, so that a lane ends with four neighbouring columns of one row of C.
+//  * MFMA: 16x16x32 bf16. The operands go in swapped, so that a lane ends with four
+//    neighbouring columns of one row of C. (fp32 with few products per operand: 4 x
+//    16x16x4.)
+//  * In the larger tiles fp32 operands are split in registers into three bf16 words,
+//    x = h + m + l: h and m round to nearest, so |m| <= 2^-9 |x|, |l| <= 2^-18 |x| and the
+//    rest is below 2^-27 |x|. The products h h', h m', m h', h l', l h', m m' leave out less
+//    than 2^-25 of |x x'|, under the 2^-24 of an fp32 rounding; sums stay in fp32. Six bf16
+//    MFMAs take 96 cycles where the fp32 ones take 256. An infinity gives NaN (inf - inf).
 //  * The gated product reads the p and the q columns of W_in as one tile and
 //    multiplies p by act(q) in registers. The backward computes them again, reads
 //    dz = dy W_out^T where the epilogue needs it, and writes dp in its place: dz is
@@ -163,15 +169,63 @@ template <typename T, bool KS, int R> struct Reader {
   }
 };
 
-// acc (16 columns n by 16 rows m) += B^T A^T over one K slice
-__device__ __forceinline__ f32x4 mma(const Frag<bf16>& n, const Frag<bf16>& m, f32x4 acc) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(n.v, m.v, acc, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mma(const Frag<float>& n, const Frag<float>& m, f32x4 acc) {
+// acc[x][y] (16 columns of block y by 16 rows of block x) += B^T A^T over one K slice
+template <int MI, int NJ>
+__device__ __forceinline__ void mma_all(const Frag<bf16> (&n)[NJ], const Frag<bf16> (&m)[MI], f32x4 (&acc)[MI][NJ]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(n.v[j], m.v[j], acc, 0, 0, 0);
-  return acc;
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n[j].v, m[i].v, acc[i][j], 0, 0, 0);
 }
+template <int MI, int NJ>
+__device__ __forceinline__ void mma_all(const Frag<float> (&n)[NJ], const Frag<float> (&m)[MI], f32x4 (&acc)[MI][NJ]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(n[j].v[k], m[i].v[k], acc[i][j], 0, 0, 0);
+}
+
+// Eight fp32 values as three bf16 words each, two values at a time: one packed
+// conversion, and the parts taken back as fp32 by a shift and a mask
+struct Words {
+  bf16x8 h, m, l;
+};
+__device__ __forceinline__ unsigned pack(float a, float b) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+  return __builtin_bit_cast(unsigned, bf16x2{(bf16)a, (bf16)b});
+}
+__device__ __forceinline__ Words split(const Frag<float>& a, const Frag<float>& b) {
+  typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+  u32x4 h, m, l;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float x = k < 2 ? a.v[2 * k] : b.v[2 * k - 4], y = k < 2 ? a.v[2 * k + 1] : b.v[2 * k - 3];
+    h[k] = pack(x, y);
+    x -= __uint_as_float(h[k] << 16);
+    y -= __uint_as_float(h[k] & 0xffff0000u);
+    m[k] = pack(x, y);
+    x -= __uint_as_float(m[k] << 16);
+    y -= __uint_as_float(m[k] & 0xffff0000u);
+    l[k] = pack(x, y);
+  }
+  return Words{__builtin_bit_cast(bf16x8, h), __builtin_bit_cast(bf16x8, m), __builtin_bit_cast(bf16x8, l)};
+}
+// acc[j] += B_j^T A^T, smallest terms first; neighbouring MFMAs go to different accumulators
+template <int NJ> __device__ __forceinline__ void mma_row(const Words (&n)[NJ], const Words& m, f32x4 (&acc)[NJ]) {
+#pragma unroll
+  for (int t = 0; t < 6; ++t)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const bf16x8 x = t == 0 ? n[j].l : (t == 2 || t == 3 ? n[j].m : n[j].h);
+      const bf16x8 y = t == 1 ? m.l : (t == 2 || t == 4 ? m.m : m.h);
+      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc[j], 0, 0, 0);
+    }
+}
+// fp32 tiles of a wave large enough for their splits to hide behind their products, in
+// us per K tile: 256 x 256 4.4 (the fp32 MFMA's peak rate is 6.8), 128 x 128 1.5 (1.7)
+template <typename T, int MI, int NJ> constexpr bool kSplit = sizeof(T) == 4 && MI * NJ >= 8;
 
 // At most N of this wave's loads still on their way, its LDS reads done; then the workgroup meets
 template <int N> __device__ __forceinline__ void tile_barrier() {
@@ -208,7 +262,15 @@ __device__ __forceinline__ void product(Loader<T, AKS, RA>& la, Loader<T, BKS, R
   };
   auto multiply_part = [&](const Frags& f, int i) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = mma(f.b[j], f.a[i], acc[i][j]);
+    for (int j = 0; j < NJ; ++j)
+      if constexpr (sizeof(T) == 2)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j].v, f.a[i].v, acc[i][j], 0, 0, 0);
+    if constexpr (sizeof(T) == 4)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(f.b[j].v[k], f.a[i].v[k], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
   // Tiles behind the last are asked for like any other; their offsets lie outside
@@ -218,6 +280,47 @@ __device__ __forceinline__ void product(Loader<T, AKS, RA>& la, Loader<T, BKS, R
   la.issue(smem + STAGE, K - BK);
   lb.issue(smem + STAGE + ABYTES, K - BK);
   tile_barrier<NL>();
+  if constexpr (kSplit<T, MI, NJ>) {
+    // fp32: both slices of a tile make one MFMA depth of split words. Row block i + 1
+    // is split while block i is multiplied, block i + 2 on its way from LDS.
+    char *cur = smem, *nxt = smem + STAGE;
+    for (int left = K; left > 0; left -= BK) {
+      Frag<T> raw[2][2];
+      raw[0][0] = ra.read(cur, ma, 0);
+      raw[0][1] = ra.read(cur, ma, 1);
+      Words b[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        b[j] = split(rb.read(cur + ABYTES, nb[j], 0), rb.read(cur + ABYTES, nb[j], 1));
+      Words a = split(raw[0][0], raw[0][1]);
+      raw[1][0] = ra.read(cur, ma + 1, 0);
+      raw[1][1] = ra.read(cur, ma + 1, 1);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        Words next = a;
+        if (i + 2 < MI) {
+          raw[i & 1][0] = ra.read(cur, ma + i + 2, 0);
+          raw[i & 1][1] = ra.read(cur, ma + i + 2, 1);
+        }
+        if (i + 1 < MI) next = split(raw[(i + 1) & 1][0], raw[(i + 1) & 1][1]);
+        mma_row<NJ>(b, a, acc[i]);
+#pragma unroll
+        for (int k = 0; k < 6 * NJ; ++k) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                             // one MFMA,
+          __builtin_amdgcn_sched_group_barrier(0x002, (44 + 6 * NJ - 1) / (6 * NJ), 0);  // its share of the split
+        }
+        a = next;
+      }
+      tile_barrier<0>();  // the next tile is in LDS; every wave has read all of this one
+      la.issue(cur, left - 2 * BK);
+      lb.issue(cur + ABYTES, left - 2 * BK);
+      char* t = cur;
+      cur = nxt;
+      nxt = t;
+    }
+    tile_barrier<0>();
+    return;
+  }
   Frags f0, f1;
 #pragma unroll
   for (int i = 0; i < MI; ++i) read_part(f0, smem, 0, i);
@@ -484,7 +587,8 @@ __global__ __launch_bounds__(512, 1) void ffn_few_kernel(const T* A, const T* B,
   constexpr int BK = Elem<T>::BK / 2, RING = few_ring(MB, NBT), SLICE = (MB + NBT) * 1024;
   constexpr int NO = PAIR ? NBT / 2 : NBT;  // column blocks of the output
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * NO * 16;
+  // neighbouring strips, which share the 128-byte lines of a row of W, on one XCD
+  const int n0 = xcd_tile(blockIdx.x, gridDim.x) * NO * 16;
   const int slices = (K + BK - 1) / BK, per = (slices + kFewWaves - 1) / kFewWaves;
   const int s0 = wave * per < slices ? wave * per : slices, s1 = s0 + per < slices ? s0 + per : slices;
   const long long k0 = (long long)s0 * BK;
@@ -518,10 +622,7 @@ __global__ __launch_bounds__(512, 1) void ffn_few_kernel(const T* A, const T* B,
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next loads write there
     la.issue(cur, range - (i + RING) * BK);
     lb.issue(cur + MB * 1024, range - (i + RING) * BK);
-#pragma unroll
-    for (int x = 0; x < MB; ++x)
-#pragma unroll
-      for (int y = 0; y < NBT; ++y) acc[x][y] = mma(b[y], a[x], acc[x][y]);
+    mma_all<MB, NBT>(b, a, acc);
     cur = cur + SLICE == ring + RING * SLICE ? ring : cur + SLICE;
   }
   tile_barrier<0>();
@@ -713,15 +814,15 @@ template <typename T, int ACT> hipError_t bwd_go(const FfnArgs& a, const FfnPlan
   return gemm_go<T, true, true>(p.dw_out, z, dy, static_cast<T*>(a.dw_out), a.F, a.D, a.M, a.F, a.D, a.D, a.part, s);
 }
 
-// Tile and K splits of a product by an estimate of its time. A workgroup alone on a
-// CU takes `alone` us per K tile, several take `pace` us each (measured, bf16: a 256 x
-// 256 tile 1.35, 128 x 128 0.7 alone and 0.42 together; fp32 is bound by its MFMA rate,
-// in proportion to the area); launch, first loads and stores take `fixed`; splits
-// write and read their partial sums at about 4 TB/s and add a launch.
+// Tile and K splits of a product by an estimate of its time. Measured at 4096-deep
+// products: a workgroup alone on a CU takes `alone` us per K tile of 128 bytes, several
+// share the CU at `pace` each; every round of workgroups adds `round` us of first loads
+// and stores (in proportion to the area: the stores of all CUs share HBM); splits write
+// and read their partial sums at about 4 TB/s and add a launch.
 FfnProduct choose(long long M, long long N, long long K, bool bf, bool may_split, bool gate) {
-  static const double pace_bf[] = {1.35, 1.08, 0.42, 0.26}, alone_bf[] = {1.35, 1.08, 0.70, 0.40};
-  static const double pace_f32[] = {4.0, 3.0, 1.05, 0.55}, alone_f32[] = {4.0, 3.0, 1.3, 0.8};
-  static const double fixed[] = {8, 7, 4.5, 3.5};
+  static const double pace_bf[] = {1.15, 0.92, 0.35, 0.27}, alone_bf[] = {1.15, 0.92, 0.64, 0.53};
+  static const double pace_f32[] = {4.4, 3.5, 1.5, 1.05}, alone_f32[] = {4.4, 3.5, 1.7, 1.2};
+  static const double round[] = {9, 7, 2.5, 1.5};
   const long long kt = (K + (bf ? 63 : 31)) / (bf ? 64 : 32);
   FfnProduct best{0, 1};
   double best_us = 1e30;
@@ -733,7 +834,7 @@ FfnProduct choose(long long M, long long N, long long K, bool bf, bool may_split
       if (s > 1 && (!may_split || kt / s < 4 || tiles * s > 512)) break;
       const long long rounds = (tiles * s + 255) / 256;
       const double per = rounds * pace > alone ? rounds * pace : alone;
-      double us = (kt + s - 1) / s * per + fixed[c];
+      double us = (kt + s - 1) / s * per + rounds * round[c] + 2;
       if (s > 1) us += 4 + (double)M * N * s * 8e-6 / 4;
       if (us < best_us) {
         best_us = us;
