@@ -334,8 +334,8 @@ def hyena_group_norm_bwd(x, dy, groups, mean, rstd, gamma=None, beta=None, act=A
         _tensor(t, name, (B, groups), torch.float32)
     guard, stream = _on(x, dy, gamma, beta, lens, mean, rstd, dx)
     with guard:
-        out = dict(dx=torch.empty_like(x) if dx is None else dx, dgamma=torch.empty(C, device=x.device),
-                   dbeta=torch.empty(C, device=x.device))
+        d = torch.empty(2, C, device=x.device)  # neighbours: their sums take one launch
+        out = dict(dx=torch.empty_like(x) if dx is None else dx, dgamma=d[0], dbeta=d[1])
         ws = _scratch(ws, x, "hyena_group_norm_bwd_workspace_bytes", B, S, C, groups, dt)
         _check(lib().hyena_group_norm_bwd(B, S, C, groups, dt, act, _p(x), _p(dy), _p(gamma), _p(beta), _p(lens),
                                           _p(mean), _p(rstd), _p(out["dx"]), _p(out["dgamma"]), _p(out["dbeta"]),

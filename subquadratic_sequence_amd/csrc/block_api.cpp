@@ -123,8 +123,8 @@ bool gn_shape_ok(int B, int S, int C, int G) {
 struct GnWs {
   size_t part, chan, total;
 };
-GnWs gn_ws(int B, int S, int C, int G, bool bwd) {
-  const hy::GnPlan p = hy::gn_plan(B, S, C, G);
+GnWs gn_ws(int B, int S, int C, int G, int dtype, bool bwd) {
+  const hy::GnPlan p = hy::gn_plan(B, S, C, G, dtype == HYENA_BF16);
   GnWs w{};
   size_t off = 0;
   w.part = off;
@@ -246,12 +246,12 @@ int hyena_glr_step(int B, int D, int S, int dtype, const void* v, long long v_ro
 
 size_t hyena_group_norm_workspace_bytes(int B, int S, int C, int G, int dtype) {
   if (!gn_shape_ok(B, S, C, G) || !dtype_ok(dtype)) return 0;
-  return gn_ws(B, S, C, G, false).total;
+  return gn_ws(B, S, C, G, dtype, false).total;
 }
 
 size_t hyena_group_norm_bwd_workspace_bytes(int B, int S, int C, int G, int dtype) {
   if (!gn_shape_ok(B, S, C, G) || !dtype_ok(dtype)) return 0;
-  return gn_ws(B, S, C, G, true).total;
+  return gn_ws(B, S, C, G, dtype, true).total;
 }
 
 int hyena_group_norm_fwd(int B, int S, int C, int G, int dtype, int act, float eps, const void* x, const float* gamma,
@@ -264,7 +264,7 @@ int hyena_group_norm_fwd(int B, int S, int C, int G, int dtype, int act, float e
       !aligned(lens, 4))
     return HYENA_ERR_INVALID_ARG;
   if (!gn_shape_ok(B, S, C, G)) return HYENA_ERR_UNSUPPORTED;
-  const GnWs w = gn_ws(B, S, C, G, false);
+  const GnWs w = gn_ws(B, S, C, G, dtype, false);
   if (ws_bytes < w.total) return HYENA_ERR_WORKSPACE;
   if (device_ok() != HYENA_OK) return HYENA_ERR_HIP;
   hy::GnArgs a{};
@@ -283,7 +283,7 @@ int hyena_group_norm_fwd(int B, int S, int C, int G, int dtype, int act, float e
   a.mean = mean;
   a.rstd = rstd;
   a.part = reinterpret_cast<float2*>(static_cast<char*>(ws) + w.part);
-  HY_CHECK_HIP(hy::gn_fwd(a, hy::gn_plan(B, S, C, G), dtype == HYENA_BF16, stream));
+  HY_CHECK_HIP(hy::gn_fwd(a, hy::gn_plan(B, S, C, G, dtype == HYENA_BF16), dtype == HYENA_BF16, stream));
   return HYENA_OK;
 }
 
@@ -297,7 +297,7 @@ int hyena_group_norm_bwd(int B, int S, int C, int G, int dtype, int act, const v
       !aligned16_or_null(dbeta) || !aligned(lens, 4))
     return HYENA_ERR_INVALID_ARG;
   if (!gn_shape_ok(B, S, C, G)) return HYENA_ERR_UNSUPPORTED;
-  const GnWs w = gn_ws(B, S, C, G, true);
+  const GnWs w = gn_ws(B, S, C, G, dtype, true);
   if (ws_bytes < w.total) return HYENA_ERR_WORKSPACE;
   if (device_ok() != HYENA_OK) return HYENA_ERR_HIP;
   char* wb = static_cast<char*>(ws);
@@ -319,7 +319,7 @@ int hyena_group_norm_bwd(int B, int S, int C, int G, int dtype, int act, const v
   a.dbeta = dbeta;
   a.part = reinterpret_cast<float2*>(wb + w.part);
   a.chan = reinterpret_cast<float*>(wb + w.chan);
-  HY_CHECK_HIP(hy::gn_bwd(a, hy::gn_plan(B, S, C, G), dtype == HYENA_BF16, stream));
+  HY_CHECK_HIP(hy::gn_bwd(a, hy::gn_plan(B, S, C, G, dtype == HYENA_BF16), dtype == HYENA_BF16, stream));
   return HYENA_OK;
 }
 

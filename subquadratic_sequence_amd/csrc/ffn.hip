@@ -362,6 +362,7 @@ __device__ __forceinline__ void store(bf16* p, f32x4 v) {
   *reinterpret_cast<bf16x4*>(p) = r;
 }
 
+template <typename T> using Raw4 = std::conditional_t<sizeof(T) == 2, bf16x4, f32x4>;  // four elements as stored
 __device__ __forceinline__ f32x4 load(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 __device__ __forceinline__ f32x4 load(const bf16* p) {
   const bf16x4 r = *reinterpret_cast<const bf16x4*>(p);
@@ -488,6 +489,16 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_dgate_kernel(const T* x, cons
   GatePlace<TM, TF> w(M, F, ntn);
   f32x4 acc[MI][NJ];
   w.template run<T>(x, w_in, M, D, F, acc);
+  // all of dz first (the loads overlap); places outside the matrix read their last neighbour
+  Raw4<T> g4[MI][NH];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NH; ++j) {
+      const int m = w.row(i) < M ? w.row(i) : M - 1, f = w.col(j) < F ? w.col(j) : F - 4;
+      g4[i][j] = *reinterpret_cast<const Raw4<T>*>(dpq + (size_t)m * 2 * F + f);
+    }
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int m = w.row(i);
@@ -496,7 +507,9 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_dgate_kernel(const T* x, cons
       const int f = w.col(j);
       if (m >= M || f >= F) continue;
       T* d = dpq + (size_t)m * 2 * F + f;
-      const f32x4 g = load(d);
+      f32x4 g;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) g[k] = (float)g4[i][j][k];
       f32x4 vz, vp, vq;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {

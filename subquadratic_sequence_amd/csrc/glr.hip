@@ -171,6 +171,7 @@ __global__ __launch_bounds__(256) void glr_agg_kernel(GlrArgs a, GlrPlan p) {
       if (GATE) rg.load(g, a.gr, t0, tmax);
       rd.load(dy, a.dyr, t0, tmax);
     }
+    __builtin_amdgcn_sched_barrier(0);  // all loads on their way before the first is used
     float A[4] = {1.f, 1.f, 1.f, 1.f}, X[4] = {0.f, 0.f, 0.f, 0.f}, Rr[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -192,7 +193,7 @@ __global__ __launch_bounds__(256) void glr_agg_kernel(GlrArgs a, GlrPlan p) {
         X[k] = step<MASK>(al, X[k], x);
         A[k] = MASK ? join(A[k], al) : A[k] * al;
         if (BWD) {
-          const float r = live ? dd[k] * (GATE ? silu_f(gg[k]) : 1.f) : 0.f;
+          const float r = live ? dd[k] * (GATE ? act_f<HYENA_ACT_SILU, T>(gg[k]) : 1.f) : 0.f;
           // prefix product times r_t; a reset at or before t keeps r from reaching the left end
           Rr[k] += MASK ? (A[k] == 0.f ? 0.f : A[k] * r) : A[k] * r;
         }
@@ -251,6 +252,7 @@ __global__ __launch_bounds__(256) void glr_fwd_kernel(GlrArgs a, GlrPlan p) {
     rv.load(v, a.vr, t0, tmax);
     rf.load(f, a.fr, t0, tmax);
     if (GATE) rg.load(g, a.gr, t0, tmax);
+    __builtin_amdgcn_sched_barrier(0);
     float al[R][4], x[R][4], A[4] = {1.f, 1.f, 1.f, 1.f}, X[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -289,7 +291,7 @@ __global__ __launch_bounds__(256) void glr_fwd_kernel(GlrArgs a, GlrPlan p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         hh[k] = step<MASK>(al[i][k], hh[k], x[i][k]);
-        yy[k] = GATE ? hh[k] * silu_f(gg[k]) : hh[k];
+        yy[k] = GATE ? hh[k] * act_f<HYENA_ACT_SILU, T>(gg[k]) : hh[k];
       }
       if (MASK && t >= w.len) yy[0] = yy[1] = yy[2] = yy[3] = 0.f;
       if (w.on && t < ylen) store4(y + (long long)t * a.yr, yy);
@@ -367,6 +369,7 @@ __global__ __launch_bounds__(256) void glr_bwd_kernel(GlrArgs a, GlrPlan p) {
     if (GATE) rg.load(g, a.gr, t0, tmax);
     rd.load(dy, a.dyr, t0, tmax);
     if (carries && p.nsb_total > 1) h = subs[(size_t)sb * a.D + cch].y;
+    __builtin_amdgcn_sched_barrier(0);
     // the run's (A, X, R); c = 1 - a, r = dy silu(g), q = dy silu'(g) for the second pass
     float al[R][4], cc[R][4], rr[R][4], qq[R][4];
     float A[4] = {1.f, 1.f, 1.f, 1.f}, X[4] = {0.f, 0.f, 0.f, 0.f}, Rr[4] = {0.f, 0.f, 0.f, 0.f};
@@ -389,7 +392,7 @@ __global__ __launch_bounds__(256) void glr_bwd_kernel(GlrArgs a, GlrPlan p) {
         cc[i][k] = live ? c : 0.f;
         const float x = live ? c * vv[k] : 0.f;
         float sg = 1.f, ds = 0.f;
-        if (GATE) silu_d(gg[k], sg, ds);
+        if (GATE) act_d<HYENA_ACT_SILU, T>(gg[k], sg, ds);
         rr[i][k] = live ? dd[k] * sg : 0.f;
         qq[i][k] = live ? dd[k] * ds : 0.f;
         const float ae = MASK && rst[i] ? 0.f : al[i][k];
@@ -526,7 +529,7 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrStepArgs a) {
       float gg[4];
       unpack(*reinterpret_cast<const typename Raw4<T>::type*>(g + i * a.gr), gg);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) yy[k] *= silu_f(gg[k]);
+      for (int k = 0; k < 4; ++k) yy[k] *= act_f<HYENA_ACT_SILU, T>(gg[k]);
     }
     store4(y + i * a.yr, yy);
     if (!later) break;

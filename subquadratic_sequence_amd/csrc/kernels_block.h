@@ -79,16 +79,17 @@ struct GnArgs {
 // How the rows of a sample are dealt out.
 //   rows form (S = 1, C / G a multiple of 8): `lanes` lanes of `nv` vectors of 8
 //   channels per group, `slots` samples side by side, `per` samples per workgroup;
-//   otherwise `slots` rows of C / 8 threads, chunks of `per` rows
+//   otherwise `slots` rows of C / vec threads, blocks of rows dealt to `chunks`
 struct GnPlan {
   bool rows_form;
+  int vec;               // channels of a thread (general form)
   int threads, slots, per, chunks;
   int lanes, nv;         // rows form
   int group_lanes;       // lanes that reduce one group (general form)
   int samples;           // samples a workgroup of the one-chunk backward takes
   long long chan_rows;   // rows of the channel sums
 };
-GnPlan gn_plan(int B, int S, int C, int G);
+GnPlan gn_plan(int B, int S, int C, int G, bool bf16);
 hipError_t gn_fwd(const GnArgs& a, const GnPlan& p, bool bf16, hipStream_t s);
 hipError_t gn_bwd(const GnArgs& a, const GnPlan& p, bool bf16, hipStream_t s);
 

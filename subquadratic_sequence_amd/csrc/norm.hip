@@ -5,11 +5,12 @@
 //   dn = dy act'(n), dx = rstd (gamma dn - m1 - xh m2), m1 = avg(gamma dn), m2 = avg(gamma dn xh)
 //
 // Memory bound: the forward must read x and write y, the backward read x and dy
-// and write dx. A thread owns 8 neighbouring channels and walks rows, whatever
-// the groups are; groups only meet where the threads' sums do, in LDS. Variances
+// and write dx. A thread owns 16 bytes of neighbouring channels (fp32 rows of more
+// than 4096 channels: 32) and walks rows, whatever the groups are; groups only meet where the threads' sums do, in LDS. Variances
 // come from deviations: a block of rows in registers gives its own mean and
-// M2 = sum (x - mean)^2, and (n, mean, M2) triples join exactly as
-//   mean = m_a + d n_b / n,  M2 = M2_a + M2_b + d^2 n_a n_b / n,  d = m_b - m_a.
+// M2 = sum (x - mean)^2, two of them join as mean = m_a + d n_b / n, M2 = M2_a + M2_b +
+// d^2 n_a n_b / n with d = m_b - m_a, and many as mean = sum n_i m_i / n, then M2 = sum M2_i +
+// n_i (m_i - mean)^2 (two short sums instead of a chain of divisions).
 //
 //  * Samples of one row (S = 1: a norm per token) whose groups are whole
 //    vectors: a group is a few lanes of one wave, everything stays in
@@ -30,14 +31,6 @@ namespace {
 struct Moments {
   float n, mean, m2;
 };
-__device__ __forceinline__ Moments join(Moments a, Moments b) {
-  const float n = a.n + b.n;
-  const float w = n > 0.f ? b.n / n : 0.f, d = b.mean - a.mean;
-  return Moments{n, fmaf(d, w, a.mean), fmaf(d * d, a.n * w, a.m2 + b.m2)};
-}
-__device__ __forceinline__ Moments shfl_down(Moments m, int o, int w) {
-  return Moments{__shfl_down(m.n, o, w), __shfl_down(m.mean, o, w), __shfl_down(m.m2, o, w)};
-}
 
 __device__ __forceinline__ int live_rows(const int* lens, int b, int S) {
   if (!lens) return S;
@@ -45,53 +38,161 @@ __device__ __forceinline__ int live_rows(const int* lens, int b, int S) {
   return n < 0 ? 0 : (n < S ? n : S);
 }
 
-// Rows of a chunk that thread row-slot `slot` of `slots` walks: slot, slot + slots, ...
-__device__ __forceinline__ int slot_rows(int rows, int slot, int slots) {
-  return rows > slot ? (rows - slot + slots - 1) / slots : 0;
+// The rows of a sample are dealt to its chunks in blocks of `unit` (slots rows side by
+// side, N of them one after the other per thread): block i goes to chunk i mod
+// chunks, so that the workgroups of a launch read neighbouring memory at any time
+// (each with a long stretch of its own, they would meet on the same HBM channels).
+// Rows of a slot (of all slots, for slot < 0) in a chunk, of `rows` in the sample:
+__device__ __forceinline__ int dealt(int rows, int chunk, int chunks, int unit, int slot, int slots) {
+  const int full = rows / unit, rest = rows - full * unit;
+  const int mine = full > chunk ? (full - chunk + chunks - 1) / chunks : 0;
+  int n = mine * (slot < 0 ? unit : unit / slots);
+  if (full % chunks == chunk) n += slot < 0 ? rest : (rest > slot ? (rest - slot + slots - 1) / slots : 0);
+  return n;
 }
 
-constexpr int kU = 4;  // rows of a thread in flight
-
-// gamma and beta of 8 channels (1 and 0 without them)
-__device__ __forceinline__ void affine(const float* gamma, const float* beta, int c, float (&ga)[8], float (&be)[8]) {
+// V channels of a row
+template <typename T, int V> struct Raw;
+template <> struct Raw<float, 4> { float4 a; };
+template <> struct Raw<float, 8> { float4 a, b; };
+template <> struct Raw<bf16, 8> { bf16v8 a; };
+__device__ __forceinline__ void unpack(const Raw<float, 4>& r, float (&v)[4]) {
+  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+}
+__device__ __forceinline__ void unpack(const Raw<float, 8>& r, float (&v)[8]) {
+  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+  v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+__device__ __forceinline__ void unpack(const Raw<bf16, 8>& r, float (&v)[8]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < 8; ++k) v[k] = (float)r.a[k];
+}
+__device__ __forceinline__ void put(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <typename T> __device__ __forceinline__ void put(T* p, const float (&v)[8]) { st8(p, v); }
+
+// Rows of a thread in flight (64 to 128 bytes of each tensor)
+constexpr int rows_ahead(int v) { return v == 4 ? 8 : 4; }
+
+// gamma and beta of V channels (1 and 0 without them)
+template <int V>
+__device__ __forceinline__ void affine(const float* gamma, const float* beta, int c, float (&ga)[V], float (&be)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
     ga[k] = 1.f;
     be[k] = 0.f;
   }
-  if (gamma) ld8(gamma + c, ga);
-  if (beta) ld8(beta + c, be);
+  if (gamma) unpack(*reinterpret_cast<const Raw<float, V>*>(gamma + c), ga);
+  if (beta) unpack(*reinterpret_cast<const Raw<float, V>*>(beta + c), be);
 }
 
 // A workgroup's place in the general form
 struct Place {
-  int b, chunk, slot, c, r0, rows;  // rows: live rows of the chunk
+  int b, chunk, slot, c, rows;  // rows: live rows of the sample
+  unsigned off;                 // elements from a block's first row to the thread's first
+  size_t at, step;              // elements to the sample, between a thread's rows
   bool on;
 };
+template <int V>
 __device__ __forceinline__ Place place(const GnArgs& a, const GnPlan& p, int b, int chunk) {
   Place w;
   w.chunk = chunk;
   w.b = b;
-  const int nv = a.C >> 3;
+  const int nv = a.C / V;
   w.slot = threadIdx.x / nv;
-  w.c = (threadIdx.x - w.slot * nv) * 8;
+  w.c = (threadIdx.x - w.slot * nv) * V;
   w.on = w.slot < p.slots;
-  w.r0 = w.chunk * p.per;
-  const int left = live_rows(a.lens, w.b, a.S) - w.r0;
-  w.rows = left < 0 ? 0 : (left < p.per ? left : p.per);
+  w.rows = live_rows(a.lens, w.b, a.S);
+  w.off = (unsigned)(w.slot * a.C + w.c);
+  w.at = (size_t)w.b * a.S * a.C;
+  w.step = (size_t)p.slots * a.C;
   return w;
 }
+// Walks a thread's rows below `rows`, a block at a time: load(raw, at, n) and
+// use(raw, at, n), at the elements from the sample to the block, n how many of the
+// block's N rows per thread there are. The next block is on its way while one is
+// used. A block's address is uniform: a load costs no vector address of its own.
+template <int N, typename R, typename Load, typename Use>
+__device__ __forceinline__ void walk(const GnPlan& p, const Place& w, int rows, int C, Load load, Use use) {
+  const int unit = p.slots * N, full = rows / unit, rest = rows - full * unit;
+  auto at = [&](int i) { return (size_t)i * unit * C; };
+  R a, b;
+  int i = w.chunk;
+  if (i < full) load(a, at(i), N);
+  while (i < full) {
+    const int j = i + p.chunks;
+    if (j < full) load(b, at(j), N);
+    __builtin_amdgcn_sched_barrier(0);  // (the compiler would move the loads down to their use)
+    use(a, at(i), N);
+    i = j;
+    if (j >= full) break;
+    const int k = j + p.chunks;
+    if (k < full) load(a, at(k), N);
+    __builtin_amdgcn_sched_barrier(0);
+    use(b, at(j), N);
+    i = k;
+  }
+  if (i == full && w.slot < rest) {
+    const int n = (rest - w.slot + p.slots - 1) / p.slots;
+    load(a, at(i), n);
+    use(a, at(i), n);
+  }
+}
+template <typename T, int V, int N> struct Block {
+  Raw<T, V> r[N];
+};
+template <typename T, int V, int N> struct Block2 {
+  Raw<T, V> x[N], d[N];
+};
+// row u of a walk's body: rows that are not there repeat the first
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> fetch(const T* sample, const Place& w, size_t at, int u, int n) {
+  return *reinterpret_cast<const Raw<T, V>*>(sample + at + (u < n ? u : 0) * w.step + w.off);
+}
+// zeros to the thread's rows in [rows, S)
+template <int N, int V, typename T>
+__device__ __forceinline__ void pad(const GnArgs& a, const GnPlan& p, const Place& w, T* out) {
+  float zero[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) zero[k] = 0.f;
+  if (w.rows == a.S) return;
+  const int unit = p.slots * N;
+  for (int i = w.chunk; (long long)i * unit < a.S; i += p.chunks)
+    for (int u = 0; u < N; ++u) {
+      const int r = i * unit + u * p.slots + w.slot;
+      if (r >= w.rows && r < a.S) put(out + (size_t)r * a.C + w.c, zero);
+    }
+}
 
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
 // Joins entries [0, n) of every group, `lanes` lanes to a group; emit(g, m) runs
 // in one lane of each.
 template <typename Entry, typename Emit>
 __device__ __forceinline__ void join_groups(int G, int n, int lanes, Entry entry, Emit emit) {
   const int l = threadIdx.x & (lanes - 1);
   for (int g = threadIdx.x / lanes; g < G; g += blockDim.x / lanes) {
-    Moments m{0.f, 0.f, 0.f};
-    for (int i = l; i < n; i += lanes) m = join(m, entry(g, i));
-    for (int o = lanes >> 1; o; o >>= 1) m = join(m, shfl_down(m, o, lanes));
-    if (l == 0) emit(g, m);
+    float cnt = 0.f, sum = 0.f, m2 = 0.f;
+#pragma unroll 4
+    for (int i = l; i < n; i += lanes) {
+      const Moments e = entry(g, i);
+      cnt += e.n;
+      sum = fmaf(e.n, e.mean, sum);
+    }
+    cnt = lanes_sum(cnt, lanes);
+    sum = lanes_sum(sum, lanes);
+    const float mean = cnt > 0.f ? sum / cnt : 0.f;
+#pragma unroll 4
+    for (int i = l; i < n; i += lanes) {
+      const Moments e = entry(g, i);
+      const float d = e.n > 0.f ? e.mean - mean : 0.f;
+      m2 += fmaf(e.n * d, d, e.m2);
+    }
+    m2 = lanes_sum(m2, lanes);
+    if (l == 0) emit(g, Moments{cnt, mean, m2});
   }
 }
 template <typename Entry, typename Emit>
@@ -99,51 +200,47 @@ __device__ __forceinline__ void sum_groups(int G, int n, int lanes, Entry entry,
   const int l = threadIdx.x & (lanes - 1);
   for (int g = threadIdx.x / lanes; g < G; g += blockDim.x / lanes) {
     float2 m = make_float2(0.f, 0.f);
+#pragma unroll 4
     for (int i = l; i < n; i += lanes) {
       const float2 e = entry(g, i);
       m.x += e.x;
       m.y += e.y;
     }
-    for (int o = lanes >> 1; o; o >>= 1) {
-      m.x += __shfl_down(m.x, o, lanes);
-      m.y += __shfl_down(m.y, o, lanes);
-    }
+    m.x = lanes_sum(m.x, lanes);
+    m.y = lanes_sum(m.y, lanes);
     if (l == 0) emit(g, m);
   }
 }
 
 // ------------------------------------------------------------- general form
-// Moments of a chunk's groups: out(g, (mean, M2)) for every group.
+// Moments of a chunk's groups: emit(g, moments) for every group.
 // sm: [slots][C] float2
-template <typename T, typename Emit>
+template <typename T, int V, typename Emit>
 __device__ __forceinline__ void chunk_moments(const GnArgs& a, const GnPlan& p, const Place& w, float2* sm, Emit emit) {
+  constexpr int N = rows_ahead(V);
   if (w.on) {
-    float n = 0.f, mean[8], m2[8];
+    float n = 0.f, mean[V], m2[V];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) mean[k] = m2[k] = 0.f;
-    const T* x = static_cast<const T*>(a.x) + ((size_t)w.b * a.S + w.r0) * a.C + w.c;
-    for (int r = w.slot; r < w.rows; r += kU * p.slots) {
-      float v[kU][8];
-      bool ok[kU];
+    for (int k = 0; k < V; ++k) mean[k] = m2[k] = 0.f;
+    const T* x = static_cast<const T*>(a.x) + w.at;
+    auto load = [&](Block<T, V, N>& k, size_t at, int cnt) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int ru = r + u * p.slots;
-        ok[u] = ru < w.rows;
-        ld8(x + (size_t)(ok[u] ? ru : r) * a.C, v[u]);
-      }
-      float m = 0.f;
+      for (int u = 0; u < N; ++u) k.r[u] = fetch<T, V>(x, w, at, u, cnt);
+    };
+    walk<N, Block<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block<T, V, N>& blk, size_t, int cnt) {
+      float v[N][V];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) m += ok[u] ? 1.f : 0.f;
-      const float im = 1.f / m, wn = m / (n + m), wd = n * wn;
+      for (int u = 0; u < N; ++u) unpack(blk.r[u], v[u]);
+      const float m = (float)cnt, im = 1.f / m, wn = m / (n + m), wd = n * wn;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < V; ++k) {
         float s = 0.f, q = 0.f;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) s += ok[u] ? v[u][k] : 0.f;
+        for (int u = 0; u < N; ++u) s += u < cnt ? v[u][k] : 0.f;
         const float bm = s * im;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const float d = ok[u] ? v[u][k] - bm : 0.f;
+        for (int u = 0; u < N; ++u) {
+          const float d = u < cnt ? v[u][k] - bm : 0.f;
           q = fmaf(d, d, q);
         }
         const float d = bm - mean[k];
@@ -151,9 +248,9 @@ __device__ __forceinline__ void chunk_moments(const GnArgs& a, const GnPlan& p, 
         m2[k] += fmaf(d * d, wd, q);
       }
       n += m;
-    }
+    });
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sm[(size_t)w.slot * a.C + w.c + k] = make_float2(mean[k], m2[k]);
+    for (int k = 0; k < V; ++k) sm[(size_t)w.slot * a.C + w.c + k] = make_float2(mean[k], m2[k]);
   }
   __syncthreads();
   const int cg = a.C / a.G;
@@ -162,46 +259,42 @@ __device__ __forceinline__ void chunk_moments(const GnArgs& a, const GnPlan& p, 
       [&](int g, int i) {
         const int s = i / cg, c = i - s * cg;
         const float2 e = sm[(size_t)s * a.C + g * cg + c];
-        return Moments{(float)slot_rows(w.rows, s, p.slots), e.x, e.y};
+        return Moments{(float)dealt(w.rows, w.chunk, p.chunks, p.slots * N, s, p.slots), e.x, e.y};
       },
       emit);
 }
 
 // y of the chunk's rows with stat(g) = (mean, rstd)
-template <typename T, int ACT>
+template <typename T, int V, int ACT>
 __device__ __forceinline__ void chunk_apply(const GnArgs& a, const GnPlan& p, const Place& w, const float2* stat) {
+  constexpr int N = rows_ahead(V);
   if (!w.on) return;
   const int cg = a.C / a.G;
-  float ga[8], be[8], mean[8];
-  affine(a.gamma, a.beta, w.c, ga, be);
+  float ga[V], be[V], mean[V];
+  affine<V>(a.gamma, a.beta, w.c, ga, be);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < V; ++k) {
     const float2 st = stat[(w.c + k) / cg];
     mean[k] = st.x;
     ga[k] *= st.y;
   }
-  const size_t at = ((size_t)w.b * a.S + w.r0) * a.C + w.c;
-  const T* x = static_cast<const T*>(a.x) + at;
-  T* y = static_cast<T*>(a.y) + at;
-  const int left = a.S - w.r0, all = !a.pad_zero ? w.rows : (left < p.per ? left : p.per);  // rows of y to write
-  for (int r = w.slot; r < all; r += kU * p.slots) {
-    float v[kU][8];
+  const T* x = static_cast<const T*>(a.x) + w.at;
+  T* y = static_cast<T*>(a.y) + w.at;
+  auto load = [&](Block<T, V, N>& k, size_t at, int cnt) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int ru = r + u * p.slots;
-      ld8(x + (size_t)(ru < all ? ru : r) * a.C, v[u]);
+    for (int u = 0; u < N; ++u) k.r[u] = fetch<T, V>(x, w, at, u, cnt);
+  };
+  walk<N, Block<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block<T, V, N>& blk, size_t at, int cnt) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      float v[V];
+      unpack(blk.r[u], v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] = act_f<ACT, T>(fmaf(v[k] - mean[k], ga[k], be[k]));
+      if (u < cnt) put(y + at + u * w.step + w.off, v);
     }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int ru = r + u * p.slots;
-      if (ru < all) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          v[u][k] = ru < w.rows ? act_f<ACT>(fmaf(v[u][k] - mean[k], ga[k], be[k])) : 0.f;
-        st8(y + (size_t)ru * a.C, v[u]);
-      }
-    }
-  }
+  });
+  if (a.pad_zero) pad<N, V>(a, p, w, y);
 }
 
 __device__ __forceinline__ float2 stat_of(const GnArgs& a, int b, int g, Moments m) {
@@ -214,20 +307,21 @@ __device__ __forceinline__ float2 stat_of(const GnArgs& a, int b, int g, Moments
 
 extern __shared__ float2 gn_smem[];
 
-template <typename T> __global__ __launch_bounds__(1024) void gn_moments_kernel(GnArgs a, GnPlan p) {
-  const Place w = place(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
+template <typename T, int V> __global__ __launch_bounds__(1024) void gn_moments_kernel(GnArgs a, GnPlan p) {
+  const Place w = place<V>(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
   float2* out = a.part + ((size_t)w.b * p.chunks + w.chunk) * a.G;
-  chunk_moments<T>(a, p, w, gn_smem, [&](int g, Moments m) { out[g] = make_float2(m.mean, m.m2); });
+  chunk_moments<T, V>(a, p, w, gn_smem, [&](int g, Moments m) { out[g] = make_float2(m.mean, m.m2); });
 }
 
 // second launch (chunks > 1) or the whole of it (FUSED: one chunk per sample)
-template <typename T, int ACT, bool FUSED> __global__ __launch_bounds__(1024) void gn_apply_kernel(GnArgs a, GnPlan p) {
-  const Place w = place(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
+template <typename T, int V, int ACT, bool FUSED>
+__global__ __launch_bounds__(1024) void gn_apply_kernel(GnArgs a, GnPlan p) {
+  const Place w = place<V>(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
   const int cg = a.C / a.G;
   float2* stat = gn_smem;
   if (FUSED) {
     stat = gn_smem + (size_t)p.slots * a.C;
-    chunk_moments<T>(a, p, w, gn_smem, [&](int g, Moments m) { stat[g] = stat_of(a, w.b, g, m); });
+    chunk_moments<T, V>(a, p, w, gn_smem, [&](int g, Moments m) { stat[g] = stat_of(a, w.b, g, m); });
   } else {
     const float2* part = a.part + (size_t)w.b * p.chunks * a.G;
     const int live = live_rows(a.lens, w.b, a.S);
@@ -236,61 +330,61 @@ template <typename T, int ACT, bool FUSED> __global__ __launch_bounds__(1024) vo
     join_groups(
         a.G, p.chunks, p.group_lanes,
         [&](int g, int i) {
-          const int left = live - i * p.per;
-          const int rows = left < 0 ? 0 : (left < p.per ? left : p.per);
+          const int rows = dealt(live, i, p.chunks, p.slots * rows_ahead(V), -1, p.slots);
           const float2 e = part[(size_t)i * a.G + g];
           return Moments{(float)rows * cg, e.x, e.y};
         },
         [&](int g, Moments m) { stat[g] = stat_of(first, w.b, g, m); });
   }
   __syncthreads();
-  chunk_apply<T, ACT>(a, p, w, stat);
+  chunk_apply<T, V, ACT>(a, p, w, stat);
 }
 
 // Sums of a chunk: per channel (sum dn xh, sum dn) to `chan`, per group of the
 // gamma-weighted (sum gamma dn, sum gamma dn xh) to emit. `add`: on top of what chan holds.
-template <typename T, int ACT, typename Emit>
+template <typename T, int V, int ACT, typename Emit>
 __device__ __forceinline__ void chunk_sums(const GnArgs& a, const GnPlan& p, const Place& w, float2* sm, float* chan,
                                            bool add, Emit emit) {
+  constexpr int N = 4;
   const int cg = a.C / a.G;
   if (w.on) {
-    float ga[8], be[8], mean[8], rs[8], s1[8], s2[8];
-    affine(a.gamma, a.beta, w.c, ga, be);
+    float ga[V], be[V], mean[V], rs[V], s1[V], s2[V];
+    affine<V>(a.gamma, a.beta, w.c, ga, be);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < V; ++k) {
       const size_t g = (size_t)w.b * a.G + (w.c + k) / cg;
       mean[k] = a.mean_in[g];
       rs[k] = a.rstd_in[g];
       s1[k] = s2[k] = 0.f;
     }
-    const size_t at = ((size_t)w.b * a.S + w.r0) * a.C + w.c;
-    const T* x = static_cast<const T*>(a.x) + at;
-    const T* dy = static_cast<const T*>(a.dy) + at;
-    for (int r = w.slot; r < w.rows; r += kU * p.slots) {
-      float v[kU][8], d[kU][8];
+    const T* x = static_cast<const T*>(a.x) + w.at;
+    const T* dy = static_cast<const T*>(a.dy) + w.at;
+    auto load = [&](Block2<T, V, N>& k, size_t at, int cnt) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int ru = r + u * p.slots;
-        ld8(x + (size_t)(ru < w.rows ? ru : r) * a.C, v[u]);
-        ld8(dy + (size_t)(ru < w.rows ? ru : r) * a.C, d[u]);
+      for (int u = 0; u < N; ++u) {
+        k.x[u] = fetch<T, V>(x, w, at, u, cnt);
+        k.d[u] = fetch<T, V>(dy, w, at, u, cnt);
       }
+    };
+    walk<N, Block2<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block2<T, V, N>& blk, size_t at, int cnt) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (r + u * p.slots < w.rows) {
+      for (int u = 0; u < N; ++u) {
+        float v[V], d[V];
+        unpack(blk.x[u], v);
+        unpack(blk.d[u], d);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float xh = (v[u][k] - mean[k]) * rs[k];
-            float y, da;
-            act_d<ACT>(fmaf(xh, ga[k], be[k]), y, da);
-            const float dn = d[u][k] * da;
-            s1[k] += dn;
-            s2[k] = fmaf(dn, xh, s2[k]);
-          }
+        for (int k = 0; k < V; ++k) {
+          const float xh = (v[k] - mean[k]) * rs[k];
+          float y, da;
+          act_d<ACT, T>(fmaf(xh, ga[k], be[k]), y, da);
+          const float dn = u < cnt ? d[k] * da : 0.f;
+          s1[k] += dn;
+          s2[k] = fmaf(dn, xh, s2[k]);
         }
       }
-    }
+    });
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sm[(size_t)w.slot * a.C + w.c + k] = make_float2(s1[k], s2[k]);
+    for (int k = 0; k < V; ++k) sm[(size_t)w.slot * a.C + w.c + k] = make_float2(s1[k], s2[k]);
   }
   __syncthreads();
   for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
@@ -313,61 +407,60 @@ __device__ __forceinline__ void chunk_sums(const GnArgs& a, const GnPlan& p, con
 }
 
 // dx of the chunk's rows; avg[g] = (m1, m2)
-template <typename T, int ACT>
+template <typename T, int V, int ACT>
 __device__ __forceinline__ void chunk_dx(const GnArgs& a, const GnPlan& p, const Place& w, const float2* avg) {
+  constexpr int N = 4;
   if (!w.on) return;
   const int cg = a.C / a.G;
-  float ga[8], be[8], mean[8], rs[8], m1[8], m2[8];
-  affine(a.gamma, a.beta, w.c, ga, be);
+  float ga[V], be[V], mean[V], rs[V], m1[V], m2[V];
+  affine<V>(a.gamma, a.beta, w.c, ga, be);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < V; ++k) {
     const int g = (w.c + k) / cg;
     mean[k] = a.mean_in[(size_t)w.b * a.G + g];
     rs[k] = a.rstd_in[(size_t)w.b * a.G + g];
     m1[k] = avg[g].x;
     m2[k] = avg[g].y;
   }
-  const size_t at = ((size_t)w.b * a.S + w.r0) * a.C + w.c;
-  const T* x = static_cast<const T*>(a.x) + at;
-  const T* dy = static_cast<const T*>(a.dy) + at;
-  T* dx = static_cast<T*>(a.dx) + at;
-  const int all = a.S - w.r0 < p.per ? a.S - w.r0 : p.per;  // padded rows of the chunk get zeros
-  for (int r = w.slot; r < all; r += kU * p.slots) {
-    float v[kU][8], d[kU][8];
+  const T* x = static_cast<const T*>(a.x) + w.at;
+  const T* dy = static_cast<const T*>(a.dy) + w.at;
+  T* dx = static_cast<T*>(a.dx) + w.at;
+  auto load = [&](Block2<T, V, N>& k, size_t at, int cnt) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int ru = r + u * p.slots;
-      ld8(x + (size_t)(ru < all ? ru : r) * a.C, v[u]);
-      ld8(dy + (size_t)(ru < all ? ru : r) * a.C, d[u]);
+    for (int u = 0; u < N; ++u) {
+      k.x[u] = fetch<T, V>(x, w, at, u, cnt);
+      k.d[u] = fetch<T, V>(dy, w, at, u, cnt);
     }
+  };
+  walk<N, Block2<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block2<T, V, N>& blk, size_t at, int cnt) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int ru = r + u * p.slots;
-      if (ru < all) {
+    for (int u = 0; u < N; ++u) {
+      float v[V], d[V];
+      unpack(blk.x[u], v);
+      unpack(blk.d[u], d);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float xh = (v[u][k] - mean[k]) * rs[k];
-          float y, da;
-          act_d<ACT>(fmaf(xh, ga[k], be[k]), y, da);
-          const float t = fmaf(d[u][k] * da, ga[k], -m1[k]);
-          v[u][k] = ru < w.rows ? rs[k] * fmaf(-xh, m2[k], t) : 0.f;
-        }
-        st8(dx + (size_t)ru * a.C, v[u]);
+      for (int k = 0; k < V; ++k) {
+        const float xh = (v[k] - mean[k]) * rs[k];
+        float y, da;
+        act_d<ACT, T>(fmaf(xh, ga[k], be[k]), y, da);
+        v[k] = rs[k] * fmaf(-xh, m2[k], fmaf(d[k] * da, ga[k], -m1[k]));
       }
+      if (u < cnt) put(dx + at + u * w.step + w.off, v);
     }
-  }
+  });
+  pad<N, V>(a, p, w, dx);
 }
 
-template <typename T, int ACT> __global__ __launch_bounds__(1024) void gn_sums_kernel(GnArgs a, GnPlan p) {
-  const Place w = place(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
+template <typename T, int V, int ACT> __global__ __launch_bounds__(1024) void gn_sums_kernel(GnArgs a, GnPlan p) {
+  const Place w = place<V>(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
   float2* out = a.part + ((size_t)w.b * p.chunks + w.chunk) * a.G;
   float* chan = a.chan + (size_t)blockIdx.x * 2 * a.C;
-  chunk_sums<T, ACT>(a, p, w, gn_smem, chan, false, [&](int g, float2 m) { out[g] = m; });
+  chunk_sums<T, V, ACT>(a, p, w, gn_smem, chan, false, [&](int g, float2 m) { out[g] = m; });
 }
 
 // second launch (chunks > 1): dx of one chunk
-template <typename T, int ACT> __global__ __launch_bounds__(1024) void gn_dx_kernel(GnArgs a, GnPlan p) {
-  const Place w = place(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
+template <typename T, int V, int ACT> __global__ __launch_bounds__(1024) void gn_dx_kernel(GnArgs a, GnPlan p) {
+  const Place w = place<V>(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
   const int live = live_rows(a.lens, w.b, a.S);
   const float inv = live ? 1.f / ((float)live * (float)(a.C / a.G)) : 0.f;
   float2* avg = gn_smem;
@@ -375,27 +468,30 @@ template <typename T, int ACT> __global__ __launch_bounds__(1024) void gn_dx_ker
   sum_groups(a.G, p.chunks, p.group_lanes, [&](int g, int i) { return part[(size_t)i * a.G + g]; },
              [&](int g, float2 m) { avg[g] = make_float2(m.x * inv, m.y * inv); });
   __syncthreads();
-  chunk_dx<T, ACT>(a, p, w, avg);
+  chunk_dx<T, V, ACT>(a, p, w, avg);
 }
 
 // one chunk per sample: a workgroup takes `samples` of them one after the other
-template <typename T, int ACT> __global__ __launch_bounds__(1024) void gn_bwd_kernel(GnArgs a, GnPlan p) {
+template <typename T, int V, int ACT> __global__ __launch_bounds__(1024) void gn_bwd_kernel(GnArgs a, GnPlan p) {
   float2* avg = gn_smem + (size_t)p.slots * a.C;
   float* chan = a.chan + (size_t)blockIdx.x * 2 * a.C;
   const int b0 = blockIdx.x * p.samples, b1 = b0 + p.samples < a.B ? b0 + p.samples : a.B;
   for (int b = b0; b < b1; ++b) {
-    const Place w = place(a, p, b, 0);
+    const Place w = place<V>(a, p, b, 0);
     const int live = live_rows(a.lens, b, a.S);
     const float inv = live ? 1.f / ((float)live * (float)(a.C / a.G)) : 0.f;
-    chunk_sums<T, ACT>(a, p, w, gn_smem, chan, b > b0,
+    chunk_sums<T, V, ACT>(a, p, w, gn_smem, chan, b > b0,
                        [&](int g, float2 m) { avg[g] = make_float2(m.x * inv, m.y * inv); });
     __syncthreads();
-    chunk_dx<T, ACT>(a, p, w, avg);
+    chunk_dx<T, V, ACT>(a, p, w, avg);
   }
 }
 
 // ---------------------------------------------------------------- rows form
 // One row per sample: lanes [0, LANES) of a group hold NV vectors each.
+// Threads of a workgroup, by the registers that NV vectors take
+constexpr int row_threads(int nv) { return nv == 1 ? 1024 : (nv <= 3 ? 512 : 256); }
+
 template <int NV> struct RowPlace {
   int slot, g, c0, nvec;  // first channel of the lane's first vector; vectors of the group
   int step;               // channels between its vectors
@@ -417,30 +513,24 @@ template <int NV> __device__ __forceinline__ RowPlace<NV> row_place(const GnArgs
   for (int i = 0; i < NV; ++i) w.has[i] = l + i * p.lanes < w.nvec;
   return w;
 }
-__device__ __forceinline__ float lane_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-
-template <typename T, int ACT, int NV> __global__ __launch_bounds__(1024) void gn_rows_kernel(GnArgs a, GnPlan p) {
+template <typename T, int ACT, int NV> __global__ __launch_bounds__(row_threads(NV)) void gn_rows_kernel(GnArgs a, GnPlan p) {
   const RowPlace<NV> w = row_place<NV>(a, p);
   if (!w.on) return;
   const float inv = 1.f / (float)(a.C / a.G);
   const long long b0 = (long long)blockIdx.x * p.per, b1 = b0 + p.per < a.B ? b0 + p.per : a.B;
   for (long long b = b0 + w.slot; b < b1; b += p.slots) {
     float v[NV][8];
-    const T* x = static_cast<const T*>(a.x) + b * a.C + w.c0;
     const bool live = live_rows(a.lens, (int)b, 1) == 1;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (w.has[i]) ld8(x + i * w.step, v[i]);
+      if (w.has[i]) ld8(static_cast<const T*>(a.x) + b * a.C + w.c0 + i * w.step, v[i]);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (w.has[i])
 #pragma unroll
         for (int k = 0; k < 8; ++k) s += v[i][k];
-    const float mean = lane_sum(s, p.lanes) * inv;
+    const float mean = lanes_sum(s, p.lanes) * inv;
     float q = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -450,7 +540,7 @@ template <typename T, int ACT, int NV> __global__ __launch_bounds__(1024) void g
           v[i][k] -= mean;
           q = fmaf(v[i][k], v[i][k], q);
         }
-    const float var = lane_sum(q, p.lanes) * inv;
+    const float var = lanes_sum(q, p.lanes) * inv;
     const float rstd = 1.f / sqrtf((live ? var : 0.f) + a.eps);
     if ((w.c0 - w.g * (a.C / a.G)) == 0) {
       if (a.mean) a.mean[b * a.G + w.g] = live ? mean : 0.f;
@@ -462,15 +552,15 @@ template <typename T, int ACT, int NV> __global__ __launch_bounds__(1024) void g
     for (int i = 0; i < NV; ++i)
       if (w.has[i]) {
         float ga[8], be[8];
-        affine(a.gamma, a.beta, w.c0 + i * w.step, ga, be);
+        affine<8>(a.gamma, a.beta, w.c0 + i * w.step, ga, be);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = live ? act_f<ACT>(fmaf(v[i][k] * rstd, ga[k], be[k])) : 0.f;
+        for (int k = 0; k < 8; ++k) v[i][k] = live ? act_f<ACT, T>(fmaf(v[i][k] * rstd, ga[k], be[k])) : 0.f;
         st8(y + i * w.step, v[i]);
       }
   }
 }
 
-template <typename T, int ACT, int NV> __global__ __launch_bounds__(1024) void gn_rows_dx_kernel(GnArgs a, GnPlan p) {
+template <typename T, int ACT, int NV> __global__ __launch_bounds__(row_threads(NV)) void gn_rows_dx_kernel(GnArgs a, GnPlan p) {
   const RowPlace<NV> w = row_place<NV>(a, p);
   const float inv = 1.f / (float)(a.C / a.G);
   const long long b0 = (long long)blockIdx.x * p.per, b1 = b0 + p.per < a.B ? b0 + p.per : a.B;
@@ -498,12 +588,12 @@ template <typename T, int ACT, int NV> __global__ __launch_bounds__(1024) void g
       for (int i = 0; i < NV; ++i)
         if (w.has[i]) {
           float ga[8], be[8];
-          affine(a.gamma, a.beta, w.c0 + i * w.step, ga, be);
+          affine<8>(a.gamma, a.beta, w.c0 + i * w.step, ga, be);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float xh = (v[i][k] - mean) * rstd;
             float y, da;
-            act_d<ACT>(fmaf(xh, ga[k], be[k]), y, da);
+            act_d<ACT, T>(fmaf(xh, ga[k], be[k]), y, da);
             const float dn = live ? d[i][k] * da : 0.f;
             s1[i][k] += dn;
             if (live) s2[i][k] = fmaf(dn, xh, s2[i][k]);
@@ -513,7 +603,7 @@ template <typename T, int ACT, int NV> __global__ __launch_bounds__(1024) void g
             t2 = fmaf(d[i][k], xh, t2);
           }
         }
-      const float m1 = lane_sum(t1, p.lanes) * inv, m2 = lane_sum(t2, p.lanes) * inv;
+      const float m1 = lanes_sum(t1, p.lanes) * inv, m2 = lanes_sum(t2, p.lanes) * inv;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (w.has[i]) {
@@ -597,28 +687,46 @@ template <typename T, int ACT> hipError_t rows_go(const GnArgs& a, const GnPlan&
   return hipErrorInvalidValue;
 }
 
-template <typename T, int ACT> hipError_t fwd_go(const GnArgs& a, const GnPlan& p, hipStream_t s) {
-  if (p.rows_form) return rows_go<T, ACT>(a, p, false, s);
+template <typename T, int V, int ACT> hipError_t fwd_general(const GnArgs& a, const GnPlan& p, hipStream_t s) {
   const unsigned grid = (unsigned)((long long)a.B * p.chunks);
   const size_t sums = slots_bytes(a, p), stat = (size_t)a.G * sizeof(float2);
-  if (p.chunks == 1) return launch(gn_apply_kernel<T, ACT, true>, grid, p.threads, sums + stat, a, p, s);
-  const hipError_t e = launch(gn_moments_kernel<T>, grid, p.threads, sums, a, p, s);
+  if (p.chunks == 1) return launch(gn_apply_kernel<T, V, ACT, true>, grid, p.threads, sums + stat, a, p, s);
+  const hipError_t e = launch(gn_moments_kernel<T, V>, grid, p.threads, sums, a, p, s);
   if (e != hipSuccess) return e;
-  return launch(gn_apply_kernel<T, ACT, false>, grid, p.threads, stat, a, p, s);
+  return launch(gn_apply_kernel<T, V, ACT, false>, grid, p.threads, stat, a, p, s);
+}
+
+template <typename T, int V, int ACT> hipError_t bwd_general(const GnArgs& a, const GnPlan& p, hipStream_t s) {
+  const unsigned grid = (unsigned)((long long)a.B * p.chunks);
+  const size_t sums = slots_bytes(a, p), avg = (size_t)a.G * sizeof(float2);
+  if (p.chunks == 1) return launch(gn_bwd_kernel<T, V, ACT>, (unsigned)p.chan_rows, p.threads, sums + avg, a, p, s);
+  const hipError_t e = launch(gn_sums_kernel<T, V, ACT>, grid, p.threads, sums, a, p, s);
+  if (e != hipSuccess) return e;
+  return launch(gn_dx_kernel<T, V, ACT>, grid, p.threads, avg, a, p, s);
+}
+
+template <typename T, int ACT> hipError_t fwd_go(const GnArgs& a, const GnPlan& p, hipStream_t s) {
+  if (p.rows_form) return rows_go<T, ACT>(a, p, false, s);
+  if constexpr (sizeof(T) == 4)
+    if (p.vec == 4) return fwd_general<T, 4, ACT>(a, p, s);
+  return fwd_general<T, 8, ACT>(a, p, s);
 }
 
 template <typename T, int ACT> hipError_t bwd_go(const GnArgs& a, const GnPlan& p, hipStream_t s) {
-  const unsigned grid = (unsigned)((long long)a.B * p.chunks);
-  const size_t sums = slots_bytes(a, p), avg = (size_t)a.G * sizeof(float2);
   hipError_t e;
   if (p.rows_form) {
     e = rows_go<T, ACT>(a, p, true, s);
-  } else if (p.chunks == 1) {
-    e = launch(gn_bwd_kernel<T, ACT>, (unsigned)p.chan_rows, p.threads, sums + avg, a, p, s);
   } else {
-    e = launch(gn_sums_kernel<T, ACT>, grid, p.threads, sums, a, p, s);
-    if (e == hipSuccess) e = launch(gn_dx_kernel<T, ACT>, grid, p.threads, avg, a, p, s);
+    e = hipSuccess;
+    if constexpr (sizeof(T) == 4) {
+      if (p.vec == 4) e = bwd_general<T, 4, ACT>(a, p, s);
+      else e = bwd_general<T, 8, ACT>(a, p, s);
+    } else {
+      e = bwd_general<T, 8, ACT>(a, p, s);
+    }
   }
+  // the channel sums are [rows][dgamma C, dbeta C]: one launch when they go to neighbouring outputs
+  if (e == hipSuccess && a.dgamma && a.dbeta == a.dgamma + a.C) return colsum(a.chan, a.dgamma, p.chan_rows, 2 * a.C, 2 * a.C, s);
   if (e == hipSuccess && a.dgamma) e = colsum(a.chan, a.dgamma, p.chan_rows, 2 * a.C, a.C, s);
   if (e == hipSuccess && a.dbeta) e = colsum(a.chan + a.C, a.dbeta, p.chan_rows, 2 * a.C, a.C, s);
   return e;
@@ -631,26 +739,28 @@ hipError_t colsum(const float* part, float* out, long long rows, int ld, int D, 
   return hipGetLastError();
 }
 
-GnPlan gn_plan(int B, int S, int C, int G) {
+GnPlan gn_plan(int B, int S, int C, int G, bool bf) {
   GnPlan p{};
-  const int cg = C / G, nv = C / 8;
+  p.vec = bf || C > 4096 ? 8 : 4;
+  const int cg = C / G, nv = C / p.vec;
   if (S == 1 && cg % 8 == 0) {
-    // lanes per group: the power of two (at most a wave) with the fewest idle
-    // lane-vectors, at most 16 vectors a lane; the widest among equals
-    p.rows_form = true;
+    // lanes per group, a power of two up to a wave, with `n` vectors each: few idle
+    // places and few vectors (a lane's vectors follow one another in time)
     const int q = cg / 8;
-    int best = -1;
+    double best = 1e30;
     for (int l = 64; l >= 1; l >>= 1) {
-      if (l > q && l > 1) continue;
       const int n = (q + l - 1) / l;
-      if (n > 16) continue;
-      const int waste = n * l - q;
-      if (best < 0 || waste < best) {
-        best = waste;
+      if (n > 16 || (long long)G * l > row_threads(n)) continue;
+      const double cost = (double)l * n * (1 + n / 8.0);
+      if (cost < best) {
+        best = cost;
         p.lanes = l;
         p.nv = n;
+        p.rows_form = true;
       }
     }
+  }
+  if (p.rows_form) {
     const int tps = G * p.lanes;
     p.slots = tps >= 256 ? 1 : 256 / tps;
     if ((long long)p.slots * C > 8192) p.slots = 8192 / C;  // the backward's channel sums take 64 KB of LDS at most
@@ -665,16 +775,14 @@ GnPlan gn_plan(int B, int S, int C, int G) {
   }
   p.slots = nv >= 256 ? 1 : 256 / nv;
   p.threads = (nv * p.slots + 63) / 64 * 64;
-  // about 1024 workgroups, chunks of whole register blocks of rows
+  // about 1024 workgroups; no chunk without a block of rows
   long long chunks = B >= 512 ? 1 : (1024 + B - 1) / B;
-  const int unit = p.slots * kU;
-  long long per = (S + chunks - 1) / chunks;
-  per = (per + unit - 1) / unit * unit;
-  p.per = (int)(per < S ? per : S);
-  p.chunks = (S + p.per - 1) / p.per;
-  const int n = p.chunks > 1 ? p.chunks : cg * p.slots;
+  const int unit = p.slots * rows_ahead(p.vec);
+  if (chunks > (S + unit - 1) / unit) chunks = (S + unit - 1) / unit;
+  p.chunks = (int)chunks;
+  // lanes that join a group's sums: all groups in one go
   p.group_lanes = 1;
-  while (p.group_lanes < 64 && p.group_lanes * 2 <= n) p.group_lanes *= 2;
+  while (p.group_lanes < 64 && p.group_lanes * 2 * G <= p.threads) p.group_lanes *= 2;
   // the backward's channel sums: one row per workgroup, at most 2048 of them
   p.samples = p.chunks == 1 ? (B + 2047) / 2048 : 1;
   p.chan_rows = p.chunks == 1 ? (B + p.samples - 1) / p.samples : (long long)B * p.chunks;
