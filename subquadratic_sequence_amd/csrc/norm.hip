@@ -113,30 +113,40 @@ __device__ __forceinline__ Place place(const GnArgs& a, const GnPlan& p, int b, 
 // use(raw, at, n), at the elements from the sample to the block, n how many of the
 // block's N rows per thread there are. The next block is on its way while one is
 // used. A block's address is uniform: a load costs no vector address of its own.
-template <int N, typename R, typename Load, typename Use>
+// LAST_FIRST: from the last block to the first, for a second pass over what a first
+// launch has read: its end is still in the last-level cache.
+template <int N, bool LAST_FIRST, typename R, typename Load, typename Use>
 __device__ __forceinline__ void walk(const GnPlan& p, const Place& w, int rows, int C, Load load, Use use) {
   const int unit = p.slots * N, full = rows / unit, rest = rows - full * unit;
-  auto at = [&](int i) { return (size_t)i * unit * C; };
+  const int mine = full > w.chunk ? (full - w.chunk + p.chunks - 1) / p.chunks : 0;
+  auto at = [&](int i) {
+    const int k = LAST_FIRST ? mine - 1 - i : i;
+    return (size_t)(w.chunk + (long long)k * p.chunks) * unit * C;
+  };
   R a, b;
-  int i = w.chunk;
-  if (i < full) load(a, at(i), N);
-  while (i < full) {
-    const int j = i + p.chunks;
-    if (j < full) load(b, at(j), N);
-    __builtin_amdgcn_sched_barrier(0);  // (the compiler would move the loads down to their use)
-    use(a, at(i), N);
-    i = j;
-    if (j >= full) break;
-    const int k = j + p.chunks;
-    if (k < full) load(a, at(k), N);
-    __builtin_amdgcn_sched_barrier(0);
-    use(b, at(j), N);
-    i = k;
+  int i = 0;
+  if (mine > 0) {
+    // behind the last block the loads repeat it: without branches around them the
+    // compiler's count of loads in flight stays exact
+    load(a, at(0), N);
+    for (;;) {
+      const int j = i + 1;
+      load(b, at(j < mine ? j : i), N);
+      __builtin_amdgcn_sched_barrier(0);  // (the compiler would move the loads down to their use)
+      use(a, at(i), N);
+      if (j >= mine) break;
+      i = j + 1;
+      load(a, at(i < mine ? i : j), N);
+      __builtin_amdgcn_sched_barrier(0);
+      use(b, at(j), N);
+      if (i >= mine) break;
+    }
   }
-  if (i == full && w.slot < rest) {
+  if (full % p.chunks == w.chunk && w.slot < rest) {
     const int n = (rest - w.slot + p.slots - 1) / p.slots;
-    load(a, at(i), n);
-    use(a, at(i), n);
+    const size_t end = (size_t)full * unit * C;
+    load(a, end, n);
+    use(a, end, n);
   }
 }
 template <typename T, int V, int N> struct Block {
@@ -227,7 +237,7 @@ __device__ __forceinline__ void chunk_moments(const GnArgs& a, const GnPlan& p, 
 #pragma unroll
       for (int u = 0; u < N; ++u) k.r[u] = fetch<T, V>(x, w, at, u, cnt);
     };
-    walk<N, Block<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block<T, V, N>& blk, size_t, int cnt) {
+    walk<N, false, Block<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block<T, V, N>& blk, size_t, int cnt) {
       float v[N][V];
 #pragma unroll
       for (int u = 0; u < N; ++u) unpack(blk.r[u], v[u]);
@@ -284,7 +294,7 @@ __device__ __forceinline__ void chunk_apply(const GnArgs& a, const GnPlan& p, co
 #pragma unroll
     for (int u = 0; u < N; ++u) k.r[u] = fetch<T, V>(x, w, at, u, cnt);
   };
-  walk<N, Block<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block<T, V, N>& blk, size_t at, int cnt) {
+  walk<N, true, Block<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block<T, V, N>& blk, size_t at, int cnt) {
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       float v[V];
@@ -307,15 +317,15 @@ __device__ __forceinline__ float2 stat_of(const GnArgs& a, int b, int g, Moments
 
 extern __shared__ float2 gn_smem[];
 
-template <typename T, int V> __global__ __launch_bounds__(1024) void gn_moments_kernel(GnArgs a, GnPlan p) {
+template <typename T, int V, int TPB> __global__ __launch_bounds__(TPB) void gn_moments_kernel(GnArgs a, GnPlan p) {
   const Place w = place<V>(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
   float2* out = a.part + ((size_t)w.b * p.chunks + w.chunk) * a.G;
   chunk_moments<T, V>(a, p, w, gn_smem, [&](int g, Moments m) { out[g] = make_float2(m.mean, m.m2); });
 }
 
 // second launch (chunks > 1) or the whole of it (FUSED: one chunk per sample)
-template <typename T, int V, int ACT, bool FUSED>
-__global__ __launch_bounds__(1024) void gn_apply_kernel(GnArgs a, GnPlan p) {
+template <typename T, int V, int ACT, bool FUSED, int TPB>
+__global__ __launch_bounds__(TPB) void gn_apply_kernel(GnArgs a, GnPlan p) {
   const Place w = place<V>(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
   const int cg = a.C / a.G;
   float2* stat = gn_smem;
@@ -342,10 +352,10 @@ __global__ __launch_bounds__(1024) void gn_apply_kernel(GnArgs a, GnPlan p) {
 
 // Sums of a chunk: per channel (sum dn xh, sum dn) to `chan`, per group of the
 // gamma-weighted (sum gamma dn, sum gamma dn xh) to emit. `add`: on top of what chan holds.
-template <typename T, int V, int ACT, typename Emit>
+template <typename T, int V, int ACT, int TPB, typename Emit>
 __device__ __forceinline__ void chunk_sums(const GnArgs& a, const GnPlan& p, const Place& w, float2* sm, float* chan,
                                            bool add, Emit emit) {
-  constexpr int N = 4;
+  constexpr int N = TPB > 256 ? 1 : 4;  // (wide rows: large workgroups, few registers a thread)
   const int cg = a.C / a.G;
   if (w.on) {
     float ga[V], be[V], mean[V], rs[V], s1[V], s2[V];
@@ -366,7 +376,7 @@ __device__ __forceinline__ void chunk_sums(const GnArgs& a, const GnPlan& p, con
         k.d[u] = fetch<T, V>(dy, w, at, u, cnt);
       }
     };
-    walk<N, Block2<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block2<T, V, N>& blk, size_t at, int cnt) {
+    walk<N, false, Block2<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block2<T, V, N>& blk, size_t at, int cnt) {
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         float v[V], d[V];
@@ -407,9 +417,9 @@ __device__ __forceinline__ void chunk_sums(const GnArgs& a, const GnPlan& p, con
 }
 
 // dx of the chunk's rows; avg[g] = (m1, m2)
-template <typename T, int V, int ACT>
+template <typename T, int V, int ACT, int TPB>
 __device__ __forceinline__ void chunk_dx(const GnArgs& a, const GnPlan& p, const Place& w, const float2* avg) {
-  constexpr int N = 4;
+  constexpr int N = TPB > 256 ? 1 : 4;  // (wide rows: large workgroups, few registers a thread)
   if (!w.on) return;
   const int cg = a.C / a.G;
   float ga[V], be[V], mean[V], rs[V], m1[V], m2[V];
@@ -432,7 +442,7 @@ __device__ __forceinline__ void chunk_dx(const GnArgs& a, const GnPlan& p, const
       k.d[u] = fetch<T, V>(dy, w, at, u, cnt);
     }
   };
-  walk<N, Block2<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block2<T, V, N>& blk, size_t at, int cnt) {
+  walk<N, true, Block2<T, V, N>>(p, w, w.rows, a.C, load, [&](const Block2<T, V, N>& blk, size_t at, int cnt) {
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       float v[V], d[V];
@@ -451,15 +461,15 @@ __device__ __forceinline__ void chunk_dx(const GnArgs& a, const GnPlan& p, const
   pad<N, V>(a, p, w, dx);
 }
 
-template <typename T, int V, int ACT> __global__ __launch_bounds__(1024) void gn_sums_kernel(GnArgs a, GnPlan p) {
+template <typename T, int V, int ACT, int TPB> __global__ __launch_bounds__(TPB) void gn_sums_kernel(GnArgs a, GnPlan p) {
   const Place w = place<V>(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
   float2* out = a.part + ((size_t)w.b * p.chunks + w.chunk) * a.G;
   float* chan = a.chan + (size_t)blockIdx.x * 2 * a.C;
-  chunk_sums<T, V, ACT>(a, p, w, gn_smem, chan, false, [&](int g, float2 m) { out[g] = m; });
+  chunk_sums<T, V, ACT, TPB>(a, p, w, gn_smem, chan, false, [&](int g, float2 m) { out[g] = m; });
 }
 
 // second launch (chunks > 1): dx of one chunk
-template <typename T, int V, int ACT> __global__ __launch_bounds__(1024) void gn_dx_kernel(GnArgs a, GnPlan p) {
+template <typename T, int V, int ACT, int TPB> __global__ __launch_bounds__(TPB) void gn_dx_kernel(GnArgs a, GnPlan p) {
   const Place w = place<V>(a, p, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
   const int live = live_rows(a.lens, w.b, a.S);
   const float inv = live ? 1.f / ((float)live * (float)(a.C / a.G)) : 0.f;
@@ -468,11 +478,11 @@ template <typename T, int V, int ACT> __global__ __launch_bounds__(1024) void gn
   sum_groups(a.G, p.chunks, p.group_lanes, [&](int g, int i) { return part[(size_t)i * a.G + g]; },
              [&](int g, float2 m) { avg[g] = make_float2(m.x * inv, m.y * inv); });
   __syncthreads();
-  chunk_dx<T, V, ACT>(a, p, w, avg);
+  chunk_dx<T, V, ACT, TPB>(a, p, w, avg);
 }
 
 // one chunk per sample: a workgroup takes `samples` of them one after the other
-template <typename T, int V, int ACT> __global__ __launch_bounds__(1024) void gn_bwd_kernel(GnArgs a, GnPlan p) {
+template <typename T, int V, int ACT, int TPB> __global__ __launch_bounds__(TPB) void gn_bwd_kernel(GnArgs a, GnPlan p) {
   float2* avg = gn_smem + (size_t)p.slots * a.C;
   float* chan = a.chan + (size_t)blockIdx.x * 2 * a.C;
   const int b0 = blockIdx.x * p.samples, b1 = b0 + p.samples < a.B ? b0 + p.samples : a.B;
@@ -480,10 +490,10 @@ template <typename T, int V, int ACT> __global__ __launch_bounds__(1024) void gn
     const Place w = place<V>(a, p, b, 0);
     const int live = live_rows(a.lens, b, a.S);
     const float inv = live ? 1.f / ((float)live * (float)(a.C / a.G)) : 0.f;
-    chunk_sums<T, V, ACT>(a, p, w, gn_smem, chan, b > b0,
+    chunk_sums<T, V, ACT, TPB>(a, p, w, gn_smem, chan, b > b0,
                        [&](int g, float2 m) { avg[g] = make_float2(m.x * inv, m.y * inv); });
     __syncthreads();
-    chunk_dx<T, V, ACT>(a, p, w, avg);
+    chunk_dx<T, V, ACT, TPB>(a, p, w, avg);
   }
 }
 
@@ -687,29 +697,34 @@ template <typename T, int ACT> hipError_t rows_go(const GnArgs& a, const GnPlan&
   return hipErrorInvalidValue;
 }
 
-template <typename T, int V, int ACT> hipError_t fwd_general(const GnArgs& a, const GnPlan& p, hipStream_t s) {
+template <typename T, int V, int ACT, int TPB> hipError_t fwd_general(const GnArgs& a, const GnPlan& p, hipStream_t s) {
   const unsigned grid = (unsigned)((long long)a.B * p.chunks);
   const size_t sums = slots_bytes(a, p), stat = (size_t)a.G * sizeof(float2);
-  if (p.chunks == 1) return launch(gn_apply_kernel<T, V, ACT, true>, grid, p.threads, sums + stat, a, p, s);
-  const hipError_t e = launch(gn_moments_kernel<T, V>, grid, p.threads, sums, a, p, s);
+  if (p.chunks == 1) return launch(gn_apply_kernel<T, V, ACT, true, TPB>, grid, p.threads, sums + stat, a, p, s);
+  const hipError_t e = launch(gn_moments_kernel<T, V, TPB>, grid, p.threads, sums, a, p, s);
   if (e != hipSuccess) return e;
-  return launch(gn_apply_kernel<T, V, ACT, false>, grid, p.threads, stat, a, p, s);
+  return launch(gn_apply_kernel<T, V, ACT, false, TPB>, grid, p.threads, stat, a, p, s);
 }
 
-template <typename T, int V, int ACT> hipError_t bwd_general(const GnArgs& a, const GnPlan& p, hipStream_t s) {
+template <typename T, int V, int ACT, int TPB> hipError_t bwd_general(const GnArgs& a, const GnPlan& p, hipStream_t s) {
   const unsigned grid = (unsigned)((long long)a.B * p.chunks);
   const size_t sums = slots_bytes(a, p), avg = (size_t)a.G * sizeof(float2);
-  if (p.chunks == 1) return launch(gn_bwd_kernel<T, V, ACT>, (unsigned)p.chan_rows, p.threads, sums + avg, a, p, s);
-  const hipError_t e = launch(gn_sums_kernel<T, V, ACT>, grid, p.threads, sums, a, p, s);
+  if (p.chunks == 1) return launch(gn_bwd_kernel<T, V, ACT, TPB>, (unsigned)p.chan_rows, p.threads, sums + avg, a, p, s);
+  const hipError_t e = launch(gn_sums_kernel<T, V, ACT, TPB>, grid, p.threads, sums, a, p, s);
   if (e != hipSuccess) return e;
-  return launch(gn_dx_kernel<T, V, ACT>, grid, p.threads, avg, a, p, s);
+  return launch(gn_dx_kernel<T, V, ACT, TPB>, grid, p.threads, avg, a, p, s);
+}
+
+template <typename T, int V, int ACT> hipError_t general(const GnArgs& a, const GnPlan& p, bool bwd, hipStream_t s) {
+  if (p.threads <= 256) return bwd ? bwd_general<T, V, ACT, 256>(a, p, s) : fwd_general<T, V, ACT, 256>(a, p, s);
+  return bwd ? bwd_general<T, V, ACT, 1024>(a, p, s) : fwd_general<T, V, ACT, 1024>(a, p, s);
 }
 
 template <typename T, int ACT> hipError_t fwd_go(const GnArgs& a, const GnPlan& p, hipStream_t s) {
   if (p.rows_form) return rows_go<T, ACT>(a, p, false, s);
   if constexpr (sizeof(T) == 4)
-    if (p.vec == 4) return fwd_general<T, 4, ACT>(a, p, s);
-  return fwd_general<T, 8, ACT>(a, p, s);
+    if (p.vec == 4) return general<T, 4, ACT>(a, p, false, s);
+  return general<T, 8, ACT>(a, p, false, s);
 }
 
 template <typename T, int ACT> hipError_t bwd_go(const GnArgs& a, const GnPlan& p, hipStream_t s) {
@@ -719,10 +734,10 @@ template <typename T, int ACT> hipError_t bwd_go(const GnArgs& a, const GnPlan& 
   } else {
     e = hipSuccess;
     if constexpr (sizeof(T) == 4) {
-      if (p.vec == 4) e = bwd_general<T, 4, ACT>(a, p, s);
-      else e = bwd_general<T, 8, ACT>(a, p, s);
+      if (p.vec == 4) e = general<T, 4, ACT>(a, p, true, s);
+      else e = general<T, 8, ACT>(a, p, true, s);
     } else {
-      e = bwd_general<T, 8, ACT>(a, p, s);
+      e = general<T, 8, ACT>(a, p, true, s);
     }
   }
   // the channel sums are [rows][dgamma C, dbeta C]: one launch when they go to neighbouring outputs
