@@ -1,6 +1,8 @@
 /*
  * hyena.h - C ABI of libhyena.so, the forward hot path of the Hyena operator
- * and of its 3D variant on AMD Instinct MI355X (gfx950).
+ * and of its 3D variant on AMD Instinct MI355X (gfx950), and the operators that
+ * stand around it in a block: the gated linear recurrence, the gated feed-forward
+ * block and the channels-last group norm.
  *
  * The operator (Hyena Hierarchy abstract, taxoreview.com page; French summary
  * on summarizepaper.com, "Key points") interleaves implicitly parametrised long
@@ -453,6 +455,9 @@ typedef enum { HYENA_ACT_NONE = 0, HYENA_ACT_SILU = 1, HYENA_ACT_GELU = 2 /* x P
  *   dx = [dp dq] W_in^T,  dw_in = x^T [dp dq],  dw_out = z^T dy
  * with z, dz, dp and dq in the storage type, and every sum over K, rows included, in
  * fp32. The gradients have the storage type of what they belong to.
+ * fp32 products of larger sizes multiply three-word bf16 splits of their operands
+ * (2^-25 of each product is left out; sums in fp32): an infinity, or a magnitude above
+ * 3.38e38, gives NaN in the results it reaches, and magnitudes under 2^-100 lose precision.
  * Row-major and contiguous. Supported: M in [1, 2^24], D and F multiples of 8 in
  * [8, 2^16]. y (and the gradients) may not overlap the inputs.
  */

@@ -8,8 +8,9 @@ switched off for all device code.
 
     python -m subquadratic_sequence_amd.build --abi-check
 
-also links tests/abi_check.c into _build/abi_check: the host-side entry points
-(csrc/api.cpp, csrc/nd_api.cpp, csrc/noalloc.hip) rebuilt with AddressSanitizer
+also links tests/abi_check.c into _build/abi_check (and tests/abi_check_block.c into
+_build/abi_check_block): the host-side entry points (csrc/api.cpp, csrc/nd_api.cpp,
+csrc/block_api.cpp, csrc/noalloc.hip) rebuilt with AddressSanitizer
 and UndefinedBehaviorSanitizer on their host code only (every finding aborts),
 with the kernels' objects of the plain build. It runs on the CPU.
 """
@@ -63,16 +64,17 @@ def build(verbose: bool = False) -> str:
 
 
 # Host-side entry points: argument validation and size arithmetic live here.
-SANITIZED = ["api.cpp", "nd_api.cpp", "noalloc.hip"]
+SANITIZED = ["api.cpp", "nd_api.cpp", "block_api.cpp", "noalloc.hip"]
 # Sanitizers act on the host pass only (device code is built as usual).
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address,undefined", "-Xarch_host", "-fno-sanitize-recover=all",
              "-Xarch_host", "-fno-omit-frame-pointer", "-g"]
-CHECK_SRC = os.path.join(os.path.dirname(HERE), "tests", "abi_check.c")
-CHECK_OUT = os.path.join(OBJ_DIR, "abi_check")
+CHECKS = ["abi_check", "abi_check_block"]
 
 
-def build_abi_check(verbose: bool = False) -> str:
-    """Links the sanitized ABI check; the kernels' objects come from build()."""
+def build_abi_check(verbose: bool = False, name: str = "abi_check") -> str:
+    """Links the sanitized ABI check tests/<name>.c; the kernels' objects come from build()."""
+    check_src = os.path.join(os.path.dirname(HERE), "tests", name + ".c")
+    check_out = os.path.join(OBJ_DIR, name)
     plain = sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "*.cpp")))
     kernels = [os.path.join(OBJ_DIR, os.path.basename(s) + ".o") for s in plain
                if os.path.basename(s) not in SANITIZED]
@@ -87,23 +89,24 @@ def build_abi_check(verbose: bool = False) -> str:
             raise RuntimeError(f"sanitized build failed for {name}:\n{r.stderr}")
         objs.append(obj)
     inc = os.path.join(os.path.dirname(HERE), "include")
-    main_obj = os.path.join(OBJ_DIR, "abi_check.o")
+    main_obj = os.path.join(OBJ_DIR, name + ".o")
     cmd = [HIPCC, "-x", "c", "-std=c11", "-Wall", "-Werror", *SAN_FLAGS, "-I", inc, "-I", ROCM_INC,
-           "-D__HIP_PLATFORM_AMD__", "-c", CHECK_SRC, "-o", main_obj]
+           "-D__HIP_PLATFORM_AMD__", "-c", check_src, "-o", main_obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"abi_check.c failed to compile:\n{r.stderr}")
-    cmd = [HIPCC, f"--offload-arch={ARCH}", *SAN_FLAGS, "-o", CHECK_OUT, main_obj, *objs, *kernels]
+        raise RuntimeError(f"{name}.c failed to compile:\n{r.stderr}")
+    cmd = [HIPCC, f"--offload-arch={ARCH}", *SAN_FLAGS, "-o", check_out, main_obj, *objs, *kernels]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"abi_check link failed:\n{r.stderr}")
+        raise RuntimeError(f"{name} link failed:\n{r.stderr}")
     if verbose:
-        print(f"built {CHECK_OUT}")
-    return CHECK_OUT
+        print(f"built {check_out}")
+    return check_out
 
 
 if __name__ == "__main__":
     build(verbose=True)
     if "--abi-check" in sys.argv[1:]:
-        build_abi_check(verbose=True)
+        for check in CHECKS:
+            build_abi_check(verbose=True, name=check)
     sys.exit(0)
