@@ -453,8 +453,8 @@ typedef enum { HYENA_ACT_NONE = 0, HYENA_ACT_SILU = 1, HYENA_ACT_GELU = 2 /* x P
  * Backward, p and q recomputed from x:
  *   dz = dy W_out^T, dp = dz act(q), dq = dz p act'(q)
  *   dx = [dp dq] W_in^T,  dw_in = x^T [dp dq],  dw_out = z^T dy
- * with z, dz, dp and dq in the storage type, and every sum over K, rows included, in
- * fp32. The gradients have the storage type of what they belong to.
+ * with z, dp and dq rounded once to the storage type, dz to at least 17 bits, and every
+ * sum over K, rows included, in fp32. The gradients have the storage type of what they belong to.
  * fp32 products of larger sizes multiply three-word bf16 splits of their operands
  * (2^-25 of each product is left out; sums in fp32): an infinity, or a magnitude above
  * 3.38e38, gives NaN in the results it reaches, and magnitudes under 2^-100 lose precision.

@@ -27,10 +27,10 @@
 //    MFMAs take 96 cycles where the fp32 ones take 256. An infinity gives NaN (inf - inf).
 //  * The gated product reads the p and the q columns of W_in as one tile and
 //    multiplies p by act(q) in registers. The backward computes them again, reads
-//    dz = dy W_out^T where the epilogue needs it, and writes dp in its place: dz is
-//    rounded once to the storage type on the way. (Holding dz in a third
-//    accumulator instead left tiles of half the size: 268 us against 45 + 105 us at
-//    16384 x 768 x 2048.)
+//    dz = dy W_out^T where the epilogue needs it, and writes dp and dq in its place.
+//    In bf16 dz waits there as two words (dz to 2^-17), so that dp and dq are rounded
+//    once; one word, rounded, made the gradients' error 1.7 times one rounding's
+//    instead of 1.4.
 #include <type_traits>
 
 #include "act.h"
@@ -362,6 +362,21 @@ __device__ __forceinline__ void store(bf16* p, f32x4 v) {
   *reinterpret_cast<bf16x4*>(p) = r;
 }
 
+// With lo != 0 what the rounding leaves goes lo elements further on, as a second bf16 word
+__device__ __forceinline__ void store_words(float* p, long long, f32x4 v) { store(p, v); }
+__device__ __forceinline__ void store_words(bf16* p, long long lo, f32x4 v) {
+  store(p, v);
+  if (lo) {
+    f32x4 l;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float h = (float)(bf16)v[k];
+      l[k] = fabsf(h) == INFINITY ? 0.f : v[k] - h;
+    }
+    store(p + lo, l);
+  }
+}
+
 template <typename T> using Raw4 = std::conditional_t<sizeof(T) == 2, bf16x4, f32x4>;  // four elements as stored
 __device__ __forceinline__ f32x4 load(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 __device__ __forceinline__ f32x4 load(const bf16* p) {
@@ -394,8 +409,8 @@ extern __shared__ char ffn_smem[];
 // into out + s M N in fp32
 template <typename T, typename O, bool AKS, bool BKS, int TM, int TN>
 __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_kernel(const T* A, const T* B, O* C, int M, int N, int K,
-                                                            long long lda, long long ldb, long long ldc, int ntn,
-                                                            int per) {
+                                                            long long lda, long long ldb, long long ldc,
+                                                            long long lo, int ntn, int per) {
   constexpr int MI = TM / kWm / 16, NJ = TN / kWn / 16, BK = Elem<T>::BK;
   const int tile = xcd_tile(blockIdx.x, gridDim.x);
   int tm, tn;
@@ -421,7 +436,7 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_kernel(const T* A, const
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int n = n0 + nb[j] * 16 + (lane >> 4) * 4;
-      if (m < M && n < N) store(C + m * ldc + n, acc[i][j]);
+      if (m < M && n < N) store_words(C + m * ldc + n, lo, acc[i][j]);
     }
   }
 }
@@ -490,13 +505,16 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_dgate_kernel(const T* x, cons
   f32x4 acc[MI][NJ];
   w.template run<T>(x, w_in, M, D, F, acc);
   // all of dz first (the loads overlap); places outside the matrix read their last neighbour
-  Raw4<T> g4[MI][NH];
+  constexpr int W = sizeof(T) == 2 ? 2 : 1;  // words of dz
+  Raw4<T> g4[MI][NH][W];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NH; ++j) {
       const int m = w.row(i) < M ? w.row(i) : M - 1, f = w.col(j) < F ? w.col(j) : F - 4;
-      g4[i][j] = *reinterpret_cast<const Raw4<T>*>(dpq + (size_t)m * 2 * F + f);
+#pragma unroll
+      for (int k = 0; k < W; ++k)
+        g4[i][j][k] = *reinterpret_cast<const Raw4<T>*>(dpq + (size_t)m * 2 * F + k * F + f);
     }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -509,7 +527,10 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_dgate_kernel(const T* x, cons
       T* d = dpq + (size_t)m * 2 * F + f;
       f32x4 g;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) g[k] = (float)g4[i][j][k];
+      for (int k = 0; k < 4; ++k) {
+        g[k] = (float)g4[i][j][0][k];
+        if constexpr (W == 2) g[k] += (float)g4[i][j][1][k];
+      }
       f32x4 vz, vp, vq;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -595,7 +616,8 @@ constexpr size_t few_lds(int mb, int nbt) {
 // kDgate: C = z [M][N], dpq [M][2N]
 template <typename T, bool BKS, int MODE, int ACT, int MB, int NBT>
 __global__ __launch_bounds__(512, 1) void ffn_few_kernel(const T* A, const T* B, T* C, T* dpq, int M, int N, int K,
-                                                         long long lda, long long ldb, long long ldc) {
+                                                         long long lda, long long ldb, long long ldc,
+                                                         long long lo) {
   constexpr bool PAIR = MODE != kStore;
   constexpr int BK = Elem<T>::BK / 2, RING = few_ring(MB, NBT), SLICE = (MB + NBT) * 1024;
   constexpr int NO = PAIR ? NBT / 2 : NBT;  // column blocks of the output
@@ -659,7 +681,7 @@ __global__ __launch_bounds__(512, 1) void ffn_few_kernel(const T* A, const T* B,
     if (m >= M || n >= N) continue;
     const f32x4 p = joined(m, c);
     if constexpr (MODE == kStore) {
-      store(C + m * ldc + n, p);
+      store_words(C + m * ldc + n, lo, p);
     } else {
       const f32x4 q = joined(m, NO * 16 + c);
       f32x4 z;
@@ -668,7 +690,8 @@ __global__ __launch_bounds__(512, 1) void ffn_few_kernel(const T* A, const T* B,
         for (int k = 0; k < 4; ++k) z[k] = p[k] * act_f<ACT, T>(q[k]);
       } else {
         T* d = dpq + (size_t)m * 2 * N + n;
-        const f32x4 g = load(d);
+        f32x4 g = load(d);
+        if constexpr (sizeof(T) == 2) g += load(d + N);
         f32x4 vp, vq;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -712,7 +735,7 @@ constexpr int kTm[] = {256, 256, 128, 64}, kTn[] = {256, 192, 128, 128};  // blo
 
 template <typename T, bool AKS, bool BKS, int TM, int TN>
 hipError_t gemm_tiles(const T* A, const T* B, T* C, int M, int N, int K, long long lda, long long ldb, long long ldc,
-                      int splits, float* part, hipStream_t s) {
+                      long long lo, int splits, float* part, hipStream_t s) {
   constexpr size_t lds = lds_bytes(TM, TN);
   const int ntn = (N + TN - 1) / TN, ntm = (M + TM - 1) / TM, tiles = (K + Elem<T>::BK - 1) / Elem<T>::BK;
   const int per = (tiles + splits - 1) / splits;
@@ -720,13 +743,13 @@ hipError_t gemm_tiles(const T* A, const T* B, T* C, int M, int N, int K, long lo
   if (splits == 1) {
     constexpr auto k = ffn_gemm_kernel<T, T, AKS, BKS, TM, TN>;
     if ((e = allow_lds<k>(lds)) != hipSuccess) return e;
-    k<<<dim3(ntm * ntn), kThreads, lds, s>>>(A, B, C, M, N, K, lda, ldb, ldc, ntn, per);
+    k<<<dim3(ntm * ntn), kThreads, lds, s>>>(A, B, C, M, N, K, lda, ldb, ldc, lo, ntn, per);
     return hipGetLastError();
   }
   constexpr auto k = ffn_gemm_kernel<T, float, AKS, BKS, TM, TN>;
   if ((e = allow_lds<k>(lds)) != hipSuccess) return e;
   const int used = (tiles + per - 1) / per;
-  k<<<dim3(ntm * ntn, used), kThreads, lds, s>>>(A, B, part, M, N, K, lda, ldb, N, ntn, per);
+  k<<<dim3(ntm * ntn, used), kThreads, lds, s>>>(A, B, part, M, N, K, lda, ldb, N, 0, ntn, per);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const long long n4 = (long long)M * N / 4;
   ffn_join_kernel<T><<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(part, C, n4, used);
@@ -735,24 +758,24 @@ hipError_t gemm_tiles(const T* A, const T* B, T* C, int M, int N, int K, long lo
 
 template <typename T, bool BKS, int MODE, int ACT, int MB, int NBT>
 hipError_t few_launch(const T* A, const T* B, T* C, T* dpq, int M, int N, int K, long long lda, long long ldb,
-                      long long ldc, hipStream_t s) {
+                      long long ldc, long long lo, hipStream_t s) {
   constexpr size_t lds = few_lds(MB, NBT);
   constexpr auto k = ffn_few_kernel<T, BKS, MODE, ACT, MB, NBT>;
   const hipError_t e = allow_lds<k>(lds);
   if (e != hipSuccess) return e;
   const int cols = (MODE == kStore ? NBT : NBT / 2) * 16;
-  k<<<(N + cols - 1) / cols, 512, lds, s>>>(A, B, C, dpq, M, N, K, lda, ldb, ldc);
+  k<<<(N + cols - 1) / cols, 512, lds, s>>>(A, B, C, dpq, M, N, K, lda, ldb, ldc, lo);
   return hipGetLastError();
 }
 // Narrow columns while they make at most one workgroup per CU, twice the width beyond
 template <typename T, bool BKS, int MODE, int ACT>
 hipError_t few_go(const T* A, const T* B, T* C, T* dpq, int M, int N, int K, long long lda, long long ldb,
-                  long long ldc, hipStream_t s) {
+                  long long ldc, long long lo, hipStream_t s) {
   constexpr int W = MODE == kStore ? 1 : 2;
   const bool wide = N > 256 * 16;
 #define HY_FFN_FEW(MB)                                                                                     \
-  return wide ? few_launch<T, BKS, MODE, ACT, MB, 2 * W>(A, B, C, dpq, M, N, K, lda, ldb, ldc, s)          \
-              : few_launch<T, BKS, MODE, ACT, MB, W>(A, B, C, dpq, M, N, K, lda, ldb, ldc, s);
+  return wide ? few_launch<T, BKS, MODE, ACT, MB, 2 * W>(A, B, C, dpq, M, N, K, lda, ldb, ldc, lo, s)          \
+              : few_launch<T, BKS, MODE, ACT, MB, W>(A, B, C, dpq, M, N, K, lda, ldb, ldc, lo, s);
   if (M <= 16) HY_FFN_FEW(1)
   if (M <= 32) HY_FFN_FEW(2)
   HY_FFN_FEW(4)
@@ -761,14 +784,14 @@ hipError_t few_go(const T* A, const T* B, T* C, T* dpq, int M, int N, int K, lon
 
 template <typename T, bool AKS, bool BKS>
 hipError_t gemm_go(const FfnProduct& p, const T* A, const T* B, T* C, int M, int N, int K, long long lda, long long ldb,
-                   long long ldc, float* part, hipStream_t s) {
+                   long long ldc, float* part, hipStream_t s, long long lo = 0) {
   if constexpr (!AKS)
-    if (p.tile == kFew) return few_go<T, BKS, kStore, HYENA_ACT_NONE>(A, B, C, nullptr, M, N, K, lda, ldb, ldc, s);
+    if (p.tile == kFew) return few_go<T, BKS, kStore, HYENA_ACT_NONE>(A, B, C, nullptr, M, N, K, lda, ldb, ldc, lo, s);
   switch (p.tile) {
-    case 0: return gemm_tiles<T, AKS, BKS, 256, 256>(A, B, C, M, N, K, lda, ldb, ldc, p.splits, part, s);
-    case 1: return gemm_tiles<T, AKS, BKS, 256, 192>(A, B, C, M, N, K, lda, ldb, ldc, p.splits, part, s);
-    case 2: return gemm_tiles<T, AKS, BKS, 128, 128>(A, B, C, M, N, K, lda, ldb, ldc, p.splits, part, s);
-    default: return gemm_tiles<T, AKS, BKS, 64, 128>(A, B, C, M, N, K, lda, ldb, ldc, p.splits, part, s);
+    case 0: return gemm_tiles<T, AKS, BKS, 256, 256>(A, B, C, M, N, K, lda, ldb, ldc, lo, p.splits, part, s);
+    case 1: return gemm_tiles<T, AKS, BKS, 256, 192>(A, B, C, M, N, K, lda, ldb, ldc, lo, p.splits, part, s);
+    case 2: return gemm_tiles<T, AKS, BKS, 128, 128>(A, B, C, M, N, K, lda, ldb, ldc, lo, p.splits, part, s);
+    default: return gemm_tiles<T, AKS, BKS, 64, 128>(A, B, C, M, N, K, lda, ldb, ldc, lo, p.splits, part, s);
   }
 }
 
@@ -793,8 +816,8 @@ template <typename T, int ACT> hipError_t gate_go(const FfnArgs& a, int tile, bo
   if (tile == kFew) {
     const T *x = static_cast<const T*>(a.x), *w_in = static_cast<const T*>(a.w_in);
     T *z = static_cast<T*>(a.z), *dpq = static_cast<T*>(a.dpq);
-    return bwd ? few_go<T, true, kDgate, ACT>(x, w_in, z, dpq, a.M, a.F, a.D, a.D, 2LL * a.F, 0, s)
-               : few_go<T, true, kGate, ACT>(x, w_in, z, dpq, a.M, a.F, a.D, a.D, 2LL * a.F, 0, s);
+    return bwd ? few_go<T, true, kDgate, ACT>(x, w_in, z, dpq, a.M, a.F, a.D, a.D, 2LL * a.F, 0, 0, s)
+               : few_go<T, true, kGate, ACT>(x, w_in, z, dpq, a.M, a.F, a.D, a.D, 2LL * a.F, 0, 0, s);
   }
   switch (tile) {
     case 0: return gate_tiles<T, ACT, 256, 128>(a, bwd, s);
@@ -815,8 +838,9 @@ template <typename T, int ACT> hipError_t bwd_go(const FfnArgs& a, const FfnPlan
           *w_out = static_cast<const T*>(a.w_out), *dy = static_cast<const T*>(a.dy);
   T *z = static_cast<T*>(a.z), *dpq = static_cast<T*>(a.dpq);
   const long long F2 = 2LL * a.F;
-  // dz = dy W_out^T into the p half of dpq (W_out as stored is K contiguous for it)
-  hipError_t e = gemm_go<T, false, false>(p.dz, dy, w_out, dpq, a.M, a.F, a.D, a.D, a.D, F2, a.part, s);
+  // dz = dy W_out^T into the place of dpq (W_out as stored is K contiguous for it): in bf16 as two
+  // words, so that the second product with it rounds once
+  hipError_t e = gemm_go<T, false, false>(p.dz, dy, w_out, dpq, a.M, a.F, a.D, a.D, a.D, F2, a.part, s, a.F);
   if (e != hipSuccess) return e;
   if ((e = gate_go<T, ACT>(a, p.gate.tile, true, s)) != hipSuccess) return e;
   // dx = dpq W_in^T: W_in as stored is K contiguous for it

@@ -193,3 +193,37 @@ def test_captured_replayed_and_two_streams(M, D, F):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(rec, want))
+
+
+@pytest.mark.parametrize("M", [1, 64, 100, 1000, 5000])
+def test_bf16_gradients_of_the_products_are_rounded_once(M):
+    """One row's x is (1, 0, ..), the only one with a gradient, so dw_in[0] = (dp, dq) of that row
+    with nothing summed: dp = dz q, dq = dz p. dz arrives to 2^-17 (two bf16 words of 8 bits), its
+    sum of D products to D 2^-24: relative 2^-16 in all. The value before its rounding lies so
+    close to a tie in about 2^-16 * 2^8 * 2 < 1 % of the elements; a dz rounded to bf16 first
+    would differ in a quarter of them."""
+    say(f"ffn rounded once M={M}")
+    D, F = 72, 1032
+    gen = torch.Generator().manual_seed(M)
+    x, dy = torch.zeros(M, D), torch.zeros(M, D)
+    x[M - 1, 0] = 1
+    dy[M - 1] = torch.rand(D, generator=gen) + 0.5  # one sign: no cancellation in dz
+    w_in = torch.randn(D, 2 * F, generator=gen)
+    w_out = torch.rand(F, D, generator=gen) + 0.5
+    x, dy, w_in, w_out = (t.bfloat16() for t in (x, dy, w_in, w_out))
+    dz = dy[M - 1].double() @ w_out.double().t()
+    p, q = w_in[0, :F].double(), w_in[0, F:].double()
+    want = torch.cat([dz * q, dz * p]).bfloat16()
+    got = hs.hyena_ffn_bwd(*(t.cuda() for t in (x, w_in, w_out, dy)), act=hs.ACT_NONE)["dw_in"][0].cpu()
+    assert (got != want).double().mean() < 0.02
+
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_an_overflowing_dz_stays_infinite(M):
+    D, F = 64, 128
+    x = torch.ones(M, D, dtype=torch.bfloat16, device="cuda")
+    w_in = torch.full((D, 2 * F), 2.0 ** -6, dtype=torch.bfloat16, device="cuda")
+    w_out = torch.full((F, D), 2.0 ** 66, dtype=torch.bfloat16, device="cuda")
+    dy = torch.full((M, D), 2.0 ** 66, dtype=torch.bfloat16, device="cuda")
+    g = hs.hyena_ffn_bwd(x, w_in, w_out, dy, act=hs.ACT_NONE)  # dz = 2^138
+    assert torch.isposinf(g["dx"]).all() and torch.isposinf(g["dw_in"]).all()
