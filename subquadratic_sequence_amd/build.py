@@ -81,12 +81,12 @@ def build_abi_check(verbose: bool = False, name: str = "abi_check") -> str:
     if not all(os.path.exists(o) for o in kernels):
         build()
     objs = []
-    for name in SANITIZED:
-        obj = os.path.join(OBJ_DIR, name + ".san.o")
-        cmd = [HIPCC, *FLAGS, *SAN_FLAGS, "-c", os.path.join(CSRC, name), "-o", obj]
+    for src in SANITIZED:
+        obj = os.path.join(OBJ_DIR, src + ".san.o")
+        cmd = [HIPCC, *FLAGS, *SAN_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"sanitized build failed for {name}:\n{r.stderr}")
+            raise RuntimeError(f"sanitized build failed for {src}:\n{r.stderr}")
         objs.append(obj)
     inc = os.path.join(os.path.dirname(HERE), "include")
     main_obj = os.path.join(OBJ_DIR, name + ".o")
