@@ -124,7 +124,7 @@ struct GnWs {
   size_t part, chan, total;
 };
 GnWs gn_ws(int B, int S, int C, int G, int dtype, bool bwd) {
-  const hy::GnPlan p = hy::gn_plan(B, S, C, G, dtype == HYENA_BF16);
+  const hy::GnPlan p = hy::gn_plan(B, S, C, G, dtype == HYENA_BF16, bwd);
   GnWs w{};
   size_t off = 0;
   w.part = off;
@@ -283,7 +283,7 @@ int hyena_group_norm_fwd(int B, int S, int C, int G, int dtype, int act, float e
   a.mean = mean;
   a.rstd = rstd;
   a.part = reinterpret_cast<float2*>(static_cast<char*>(ws) + w.part);
-  HY_CHECK_HIP(hy::gn_fwd(a, hy::gn_plan(B, S, C, G, dtype == HYENA_BF16), dtype == HYENA_BF16, stream));
+  HY_CHECK_HIP(hy::gn_fwd(a, hy::gn_plan(B, S, C, G, dtype == HYENA_BF16, false), dtype == HYENA_BF16, stream));
   return HYENA_OK;
 }
 
@@ -319,7 +319,7 @@ int hyena_group_norm_bwd(int B, int S, int C, int G, int dtype, int act, const v
   a.dbeta = dbeta;
   a.part = reinterpret_cast<float2*>(wb + w.part);
   a.chan = reinterpret_cast<float*>(wb + w.chan);
-  HY_CHECK_HIP(hy::gn_bwd(a, hy::gn_plan(B, S, C, G, dtype == HYENA_BF16), dtype == HYENA_BF16, stream));
+  HY_CHECK_HIP(hy::gn_bwd(a, hy::gn_plan(B, S, C, G, dtype == HYENA_BF16, true), dtype == HYENA_BF16, stream));
   return HYENA_OK;
 }
 

@@ -89,7 +89,7 @@ struct GnPlan {
   int samples;           // samples a workgroup of the one-chunk backward takes
   long long chan_rows;   // rows of the channel sums
 };
-GnPlan gn_plan(int B, int S, int C, int G, bool bf16);
+GnPlan gn_plan(int B, int S, int C, int G, bool bf16, bool bwd);
 hipError_t gn_fwd(const GnArgs& a, const GnPlan& p, bool bf16, hipStream_t s);
 hipError_t gn_bwd(const GnArgs& a, const GnPlan& p, bool bf16, hipStream_t s);
 

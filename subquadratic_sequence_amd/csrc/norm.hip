@@ -754,7 +754,7 @@ hipError_t colsum(const float* part, float* out, long long rows, int ld, int D, 
   return hipGetLastError();
 }
 
-GnPlan gn_plan(int B, int S, int C, int G, bool bf) {
+GnPlan gn_plan(int B, int S, int C, int G, bool bf, bool bwd) {
   GnPlan p{};
   p.vec = bf || C > 4096 ? 8 : 4;
   const int cg = C / G, nv = C / p.vec;
@@ -780,8 +780,11 @@ GnPlan gn_plan(int B, int S, int C, int G, bool bf) {
     p.slots = tps >= 256 ? 1 : 256 / tps;
     if ((long long)p.slots * C > 8192) p.slots = 8192 / C;  // the backward's channel sums take 64 KB of LDS at most
     p.threads = (tps * p.slots + 63) / 64 * 64;
-    // about 2048 workgroups
-    long long per = (B + 2047LL) / 2048;
+    // Forward: about 2048 workgroups (bf16 rows, us, with 1024 and 2048: 100k x 256 27.0 and 21.0).
+    // Backward: about 512, each of which leaves a row of channel sums to be added up (with 512
+    // and 2048: 16k x 768 27.8 and 42.2, 8192 x 2048 37.8 and 61; 100k x 256 51.6 and 40.0)
+    const int groups = bwd ? 512 : 2048;
+    long long per = ((long long)B + groups - 1) / groups;
     per = (per + p.slots - 1) / p.slots * p.slots;
     p.per = (int)per;
     p.chunks = 1;
@@ -790,8 +793,20 @@ GnPlan gn_plan(int B, int S, int C, int G, bool bf) {
   }
   p.slots = nv >= 256 ? 1 : 256 / nv;
   p.threads = (nv * p.slots + 63) / 64 * 64;
-  // about 1024 workgroups; no chunk without a block of rows
-  long long chunks = B >= 512 ? 1 : (1024 + B - 1) / B;
+  // One launch as soon as the samples give every CU a workgroup, and from half of that on if a
+  // sample is at most 512 KB (bf16 forward, us, one launch and two: 256 x 256 x 128 10.8 and 12.5,
+  // 200 x 1024 x 128 27 and 32, 64 x 256 x 512 20.3 and 15.9, 100 x 4096 x 256 154 and 112).
+  // Otherwise about 256 workgroups: each of the second launch joins its sample's chunks, so a
+  // sample cut finer costs more (256 and 1024 workgroups: 8 x 4096 x 384 21.8 and 36.2,
+  // 1 x 65536 x 512 44 and 119); but up to 8 chunks a sample while they are under about 1024, whose
+  // join is short, to even out the CUs' loads (100 x 4096 x 256, 300 and 800: 133 and 119).
+  const bool one = B >= 256 || (B >= 128 && (long long)S * C * (bf ? 2 : 4) <= (512 << 10));
+  long long chunks = 1;
+  if (!one) {
+    const long long even = (1024 + B - 1) / B < 8 ? (1024 + B - 1) / B : 8;
+    chunks = (256 + B - 1) / B > even ? (256 + B - 1) / B : even;
+  }
+  // no chunk without a block of rows
   const int unit = p.slots * rows_ahead(p.vec);
   if (chunks > (S + unit - 1) / unit) chunks = (S + unit - 1) / unit;
   p.chunks = (int)chunks;

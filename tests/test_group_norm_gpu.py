@@ -82,7 +82,9 @@ def run(d, G, act, check=True):
 SHAPES = [(5, 1, 8, 1), (33, 1, 64, 8), (300, 1, 768, 12), (40, 1, 768, 1), (7, 1, 768, 768), (9, 1, 384, 32),
           (70, 1, 24, 1), (5, 1, 8192, 1), (3, 1, 8192, 8192), (6, 1, 4104, 3), (2100, 1, 40, 5),
           (1, 2, 8, 8), (3, 17, 72, 9), (2, 64, 384, 32), (2, 1000, 128, 8), (1, 4097, 320, 10), (1, 5000, 64, 64),
-          (2, 3, 8192, 2), (2, 40, 8192, 4096), (600, 5, 64, 4), (2060, 3, 16, 2), (1, 9001, 8, 1), (4, 700, 2056, 8)]
+          (2, 3, 8192, 2), (2, 40, 8192, 4096), (600, 5, 64, 4), (2060, 3, 16, 2), (1, 9001, 8, 1), (4, 700, 2056, 8),
+          # many samples in one launch and in two, more rows than workgroups
+          (130, 40, 64, 8), (100, 300, 32, 4), (140, 2200, 64, 8), (1500, 1, 64, 8)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
