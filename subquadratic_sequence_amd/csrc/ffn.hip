@@ -30,7 +30,16 @@
 //    dz = dy W_out^T where the epilogue needs it, and writes dp and dq in its place.
 //    In bf16 dz waits there as two words (dz to 2^-17), so that dp and dq are rounded
 //    once; one word, rounded, made the gradients' error 1.7 times one rounding's
-//    instead of 1.4.
+//    instead of 1.4 and the backward of 16384 x 768 x 2048 33 of 531 us faster.
+//    Other homes for dz (backward, us, against the kept form): a third accumulator with
+//    half the tile, 2048 x 768 x 2048 107 and 116, 16384 x 768 x 2048 535 and 530,
+//    16384 x 2048 x 5632 3173 and 2940; the workgroup's own product, left in memory and
+//    taken back from cache, 326 us for what takes 88 + 206 at 16384 x 768 x 2048.
+//
+// Measured at 16384 x 768 x 2048, bf16: gate 98 us (1050 TFLOP/s), y 48 us; backward dz 88,
+// gates 206 (103 GFLOP, and 336 MB in the epilogue while the matrix units wait), dx 89
+// (1160 TFLOP/s), dw_in 99 + 12 and dw_out 77 + 6 us with the sums of their K splits. fp32,
+// 4099 x 384 x 1032: 72 + 42 us. 8 rows of 768 x 2048: 5.6 + 6.0 us.
 #include <type_traits>
 
 #include "act.h"
@@ -730,7 +739,10 @@ template <auto K> hipError_t allow_lds(size_t bytes) {
   return e;
 }
 
-constexpr int kFew = 4, kFewRows = 64;  // the tile index that stands for the few-rows kernel, its largest M
+// The tile index that stands for the few-rows kernel, and its largest M (bf16 forward, us, few
+// rows and tiles: 16 x 768 x 2048 14.4 and 16.5, 64 x 768 x 2048 16.5 and 18.0, 16 x 2048 x 5632
+// 29.6 and 36.8, 64 x 2048 x 5632 40.4 and 39.9)
+constexpr int kFew = 4, kFewRows = 64;
 constexpr int kTm[] = {256, 256, 128, 64}, kTn[] = {256, 192, 128, 128};  // block tiles of the plain product
 
 template <typename T, bool AKS, bool BKS, int TM, int TN>

@@ -17,6 +17,11 @@
 // (A, X[, R]) of each chunk, and every workgroup of the second folds those of
 // the chunks before it (behind it for mu) in order: no waiting between
 // workgroups and no order that varies.
+//
+// Measured, bf16 with a gate: 8 x 2048 x 768 forward 16 + 23 us (its four tensors once,
+// 101 MB, take 19 us at the 5.3 TB/s of a large copy), backward 25 + 50 us and 5 for
+// dbias; 1M x 256 backward 493 + 874 + 5 us, 4.3 TB/s of the 11 passes it makes. A
+// single position of 16 x 768 states takes 3.7 us on the GPU.
 #include "act.h"
 #include "kernels_block.h"
 
@@ -565,8 +570,10 @@ GlrPlan glr_plan(int B, int L, int D, bool bf16, bool bwd) {
   p.SB = p.R * kGlrSubs;
   p.nsb_total = (L + p.SB - 1) / p.SB;
   p.ctiles = (D + kGlrTile - 1) / kGlrTile;
-  // about 1024 workgroups (four per CU); at most 256 chunks, whose aggregates
-  // every workgroup folds
+  // About 1024 workgroups (four per CU); at most 256 chunks, whose aggregates every
+  // workgroup folds. bf16 with a gate, us, with 512, 1024 and 2048 workgroups:
+  // 8 x 2048 x 768 forward 51, 39, 39, backward 88, 81, 75; 65536 x 768 backward 325, 280, 299.
+  // With at most 64, 128 and 256 chunks: 1M x 256 forward 990, 742, 683.
   const long long tiles = (long long)B * p.ctiles;
   long long C = (1024 + tiles - 1) / tiles;
   if (C > 256) C = 256;

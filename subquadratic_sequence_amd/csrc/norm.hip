@@ -20,6 +20,10 @@
 //  * Few large samples: chunks of rows, one launch for the sums of every chunk,
 //    a second in which each workgroup joins the chunks' sums of its sample
 //    (a few kB from L2) and writes its rows.
+//
+// Measured: fp32, 8 x 64^2 x 384 forward 11 + 21 us (x and y once, 101 MB, take 19 us at the
+// 5.3 TB/s of a large copy); 2 x 64^3 x 128 backward 103 + 128 + 5 us, 5.8 TB/s of its five
+// passes (three are the floor: 152 us). bf16, 16384 single rows of 768: 12 us (floor 9.5).
 #include "act.h"
 #include "kernels_block.h"
 #include "vec8.h"
