@@ -129,11 +129,16 @@ def hyena_glr_fwd(v, f, g=None, bias=None, h0=None, reset=None, lens=None, y=Non
     v, f, g, y [B, L, D] (float32 or bfloat16, contiguous rows: column blocks of one
     tensor are fine); bias [D], h0 and h_last [B, D] float32; reset [B, L] uint8 or
     bool; lens [B] int32. The state after the last position goes to h_last, if
-    given. Positions behind lens are left as they are in a given y, zero otherwise."""
+    given (not h0 itself). Positions behind lens are left as they are in a given y, zero otherwise."""
     c = _glr_inputs(v, f, g, bias, h0, reset, lens, y is None)
     if y is not None:
         sy = _rows(y, "y", v.shape, v.dtype)
     _tensor(h_last, "h_last", (c.B, c.D), torch.float32)
+    # other workgroups still read the old state and rows when the first ones write
+    if h_last is not None and h_last.data_ptr() == c.h0:
+        raise ValueError("h_last may not be h0")
+    if y is not None and y.data_ptr() in (c.v, c.f, c.g):
+        raise ValueError("y may not be v, f or g")
     guard, stream = _on(v, f, g, bias, h0, reset, lens, y, h_last)
     with guard:
         if y is None:
@@ -173,8 +178,8 @@ def hyena_glr_bwd(v, f, dy, g=None, bias=None, h0=None, reset=None, lens=None, d
 
 def hyena_glr_step(state, v, f, g=None, bias=None, slots=None, state_out=None, y=None):
     """One position of B sequences: v, f, g, y [B, D]; state [S, D] float32, advanced
-    in place or into state_out. slots [B] int32: the row of state of each sequence
-    (default: row r); rows with a slot outside [0, S) are skipped (zero in a new y),
+    in place or into state_out (only the rows of state it advances). slots [B] int32: the
+    row of state of each sequence (default: row r); rows with a slot outside [0, S) are skipped (zero in a new y),
     rows that share a slot are consecutive positions of one sequence."""
     if not isinstance(v, torch.Tensor) or v.dim() != 2:
         raise ValueError("v: expected a tensor [B, D]")

@@ -221,6 +221,14 @@ def test_python_checks():
             raise AssertionError(f"case {i} was not refused")
 
 
+def test_outputs_that_are_inputs_are_refused():
+    import subquadratic_sequence_amd as hs
+    x, h = torch.zeros(2, 5, 16), torch.zeros(2, 16)
+    for kw, what in [(dict(h0=h, h_last=h), "h_last may not be h0"), (dict(y=x), "y may not be v")]:
+        with pytest.raises(ValueError, match=what):
+            hs.hyena_glr_fwd(x, x.clone(), **kw)
+
+
 def test_unsupported_sizes_raise_the_status():
     from subquadratic_sequence_amd import HyenaError, block
     for query, sizes in [("hyena_glr_workspace_bytes", (1, 4, 12, 0)), ("hyena_ffn_workspace_bytes", (1, 12, 8, 0)),
