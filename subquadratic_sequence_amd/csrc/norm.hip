@@ -6,11 +6,12 @@
 //
 // Memory bound: the forward must read x and write y, the backward read x and dy
 // and write dx. A thread owns 16 bytes of neighbouring channels (fp32 rows of more
-// than 4096 channels: 32) and walks rows, whatever the groups are; groups only meet where the threads' sums do, in LDS. Variances
-// come from deviations: a block of rows in registers gives its own mean and
-// M2 = sum (x - mean)^2, two of them join as mean = m_a + d n_b / n, M2 = M2_a + M2_b +
-// d^2 n_a n_b / n with d = m_b - m_a, and many as mean = sum n_i m_i / n, then M2 = sum M2_i +
-// n_i (m_i - mean)^2 (two short sums instead of a chain of divisions).
+// than 4096 channels: 32) and walks rows, whatever the groups are; groups only meet
+// where the threads' sums do, in LDS. Variances come from deviations: a block of rows
+// in registers gives its own mean and M2 = sum (x - mean)^2, two of them join as mean =
+// m_a + d n_b / n, M2 = M2_a + M2_b + d^2 n_a n_b / n with d = m_b - m_a, and many as
+// mean = sum n_i m_i / n, then M2 = sum M2_i + n_i (m_i - mean)^2 (two short sums
+// instead of a chain of divisions).
 //
 //  * Samples of one row (S = 1: a norm per token) whose groups are whole
 //    vectors: a group is a few lanes of one wave, everything stays in
